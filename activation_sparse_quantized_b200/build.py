@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, "libsgq.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-Xcompiler", "-fPIC",
-         "-Xcompiler", "-fvisibility=default", "-shared", "-cudart", "static"]
+         "-Xcompiler", "-fvisibility=default", "-shared", "-cudart", "static",
+         "--threads", "0"]
 
 
 def sources():

@@ -19,8 +19,9 @@ int fail_cuda(cudaError_t e)
     return SGQ_ERR_CUDA;
 }
 
-// SM count of the current device (cached), or a negative SGQ_ERR_*.
-int current_device_sms()
+} // namespace
+
+int sgq::current_device_sms()
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -43,6 +44,10 @@ int current_device_sms()
         return SGQ_ERR_DEVICE;
     return g_num_sms[dev];
 }
+
+namespace {
+
+using sgq::current_device_sms;
 
 bool aligned16(const void *p)
 {
@@ -142,10 +147,11 @@ const char *sgq_status_string(int code)
     case SGQ_ERR_GROUP: return "group size must be 32, 64 or 128";
     case SGQ_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
     case SGQ_ERR_BATCH: return "batch must be between 1 and 16";
-    case SGQ_ERR_WORKSPACE: return "workspace smaller than sgq_gemv_workspace_bytes";
+    case SGQ_ERR_WORKSPACE: return "workspace smaller than the entry point's *_workspace_bytes";
     case SGQ_ERR_ACT: return "unknown activation";
     case SGQ_ERR_CUDA: return "a CUDA call failed (see sgq_last_cuda_error)";
     case SGQ_ERR_DEVICE: return "the current device is not compute capability 10.x (B200)";
+    case SGQ_ERR_TYPE: return "unknown element type, or one that the argument does not take";
     case SGQ_ERR_TOO_LARGE: return "N exceeds SGQ_NOALLOC_MAX_N, the fixed scratch of sgq_gemv_thresh_noalloc";
     default: return "unknown sgq status";
     }

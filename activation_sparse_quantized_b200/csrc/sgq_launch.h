@@ -79,6 +79,60 @@ cudaError_t launch_finalize(const GemvProblem &p, cudaStream_t stream);
 // Records e as the last CUDA error of this thread; returns SGQ_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
 
+// SM count of the current device (cached), or a negative SGQ_ERR_*.
+int current_device_sms();
+
+// ---- the step around the projections (norm.cu, cache.cu, tree_attn.cu) ----
+
+struct NormProblem {
+    const void *a, *w_post, *gate, *resid, *w_pre;
+    void *resid_out;
+    uint16_t *x;
+    long long ld_a, ld_gate, ld_r, ld_ro, ld_x; // elements
+    int a_type, r_type, w_type;                 // SGQ_TYPE_*
+    int B, H;
+    float scale, w_offset, eps;
+};
+
+struct PlanProblem {
+    const int32_t *lens, *news, *held, *free_pages, *free_count, *depth;
+    int32_t *table, *held_out, *free_count_out, *cu_new, *pos, *req, *status;
+    int64_t *slots;
+    int R, page, num_pages, table_ld, max_tokens;
+};
+
+struct WriteProblem {
+    const uint16_t *q, *k, *v;
+    const int32_t *n_tokens, *pos;
+    const float *rope;
+    const int64_t *slots;
+    uint16_t *q_out;
+    int32_t *status;
+    long long ld_q, ld_k, ld_v, ld_qo;
+    int T, Hq, rope_len;
+    sgq_cache cache;
+};
+
+struct AttnProblem {
+    const uint16_t *q;
+    const int32_t *lens, *cu_new, *table;
+    const uint32_t *tree;
+    uint16_t *out;
+    float *lse;
+    void *workspace;
+    int32_t *status;
+    long long ld_q, ld_out;
+    int T, R, Hq, table_ld, tree_words;
+    float scale;
+    sgq_cache cache;
+};
+
+cudaError_t launch_norm(const NormProblem &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_plan(const PlanProblem &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_write(const WriteProblem &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_attn(const AttnProblem &p, int num_sms, cudaStream_t stream);
+size_t attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D);
+
 cudaError_t launch_glu(const uint16_t *gate, const uint16_t *up, uint16_t *h, long long n,
                        int act, int num_sms, cudaStream_t stream);
 

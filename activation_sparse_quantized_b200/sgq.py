@@ -26,7 +26,12 @@ SGQ_STATUS_BAD_INDEX = 2
 SGQ_STATUS_BAD_COUNT = 4
 SGQ_STATUS_TIMEOUT = 8
 SGQ_MAX_BATCH = 16
+SGQ_STATUS_NO_PAGES = 16
 SGQ_NOALLOC_MAX_N = 65536
+SGQ_TYPE_BF16 = 0
+SGQ_TYPE_F32 = 1
+SGQ_TYPE_E4M3 = 2
+SGQ_MAX_REQUESTS = 8192
 
 EXPORTS = (
     "sgq_packed_sizes", "sgq_pack", "sgq_select", "sgq_gemv_workspace_bytes", "sgq_gemv",
@@ -35,7 +40,8 @@ EXPORTS = (
     "sgq_gemv_glu_dense", "sgq_select_mask", "sgq_gemv_mask", "sgq_packed_sizes_nm",
     "sgq_pack_nm", "sgq_gemv_nm", "sgq_gemv_nm_thresh", "sgq_gemv_acc", "sgq_gemv_thresh_acc",
     "sgq_ffn_workspace_bytes", "sgq_ffn", "sgq_read_status", "sgq_debug_gemv_withhold",
-    "sgq_gemv_thresh_batch", "sgq_gemv_glu_thresh_batch",
+    "sgq_gemv_thresh_batch", "sgq_gemv_glu_thresh_batch", "sgq_cache_plan", "sgq_cache_write",
+    "sgq_tree_attn_workspace_bytes", "sgq_tree_attn", "sgq_residual_norm",
 )
 
 
@@ -73,6 +79,7 @@ def load(path: str = LIB_PATH):
 
 def _declare(lib):
     P, I, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    L = ctypes.c_longlong
     sig = {
         "sgq_packed_sizes": ([I, I, I, ctypes.POINTER(Z), ctypes.POINTER(Z)], I),
         "sgq_pack": ([P, I, I, I, P, P, P, P], I),
@@ -101,6 +108,11 @@ def _declare(lib):
         "sgq_ffn_workspace_bytes": ([I, I], Z),
         "sgq_read_status": ([P, P, I, P], I),
         "sgq_ffn": ([P, P, P, P, I, I, I, P, F, I, F, P, P, P, P, Z, P, P], I),
+        "sgq_cache_plan": ([P, P, I, I, I, P, I, P, P, P, P, P, P, I, P, P, P, P, P, P], I),
+        "sgq_cache_write": ([P, L, P, L, P, L, I, P, I, P, P, I, P, P, L, P, P, P], I),
+        "sgq_tree_attn_workspace_bytes": ([I, I, I, I, I], Z),
+        "sgq_tree_attn": ([P, L, I, I, I, P, P, P, I, P, P, I, F, P, L, P, P, Z, P, P], I),
+        "sgq_residual_norm": ([P, L, I, P, P, L, F, P, L, I, P, L, P, I, F, P, L, I, I, F, P], I),
         "sgq_status_string": ([I], ctypes.c_char_p),
         "sgq_last_cuda_error": ([], I),
         "sgq_layout_version": ([], I),
@@ -328,6 +340,132 @@ def sgq_glu(gate, up, h, B, I, act, stream=None):
 
 
 # --------------------------------------------------------------------------
+# The step around the projections: cache plan and store, tree attention, norm.
+# These wrappers check what the C ABI cannot see of a tensor: its element type
+# and that it lies on the current device.
+# --------------------------------------------------------------------------
+
+_INT32, _INT64, _FLOAT32, _BF16 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
+_WORDS = (torch.int32, torch.uint32)
+_FLOATS = {torch.bfloat16: SGQ_TYPE_BF16, torch.float32: SGQ_TYPE_F32}
+_CACHES = {torch.bfloat16: SGQ_TYPE_BF16, torch.float8_e4m3fn: SGQ_TYPE_E4M3}
+
+
+def _dev(name, t, types, dev):
+    """The address of a tensor of one of the types on device ``dev`` (None passes)."""
+    if t is None:
+        return None
+    if t.dtype not in types:
+        raise TypeError(f"{name}: element type {t.dtype}, expected {' or '.join(map(str, types))}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected the current device, cuda:{dev}")
+    return t.data_ptr()
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int),
+                ("page", ctypes.c_int), ("num_pages", ctypes.c_int), ("heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("slot_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Cache:
+    """The ``sgq_cache`` that describes a paged cache held in two tensors.
+
+    ``k`` and ``v`` are [num_pages, page, heads, dim] in bf16 or float8_e4m3fn,
+    contiguous along dim and with the same strides; any order of the other
+    dimensions is taken from the strides (heads before slots:
+    ``buf.transpose(1, 2)`` of a [num_pages, heads, page, dim] buffer). The
+    tensors are kept alive by this object.
+    """
+
+    def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("Cache: k and v must be [num_pages, page, heads, dim] alike")
+        if k.dtype not in _CACHES:
+            raise TypeError(f"Cache: element type {k.dtype}, expected bfloat16 or float8_e4m3fn")
+        if k.stride(3) != 1:
+            raise ValueError("Cache: k and v must be contiguous along dim")
+        if k.get_device() != v.get_device():
+            raise ValueError("Cache: k and v must be on one device")
+        self.k, self.v = k, v
+        self.device = k.get_device()
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _CACHES[k.dtype], k.shape[1],
+                                   k.shape[0], k.shape[2], k.shape[3], k.stride(0), k.stride(1),
+                                   k.stride(2), float(k_scale), float(v_scale))
+        self.ptr = ctypes.addressof(self.struct)
+
+    def on(self, dev):
+        if self.device != dev:
+            raise ValueError(f"cache: on device {self.device}, expected the current device, cuda:{dev}")
+        return self.ptr
+
+
+def sgq_cache_plan(lens, news, R, page, num_pages, table, table_ld, held, held_out, free_pages,
+                   free_count, free_count_out, depth, max_tokens, cu_new, slots, pos, req,
+                   status=None, stream=None):
+    """Block tables, slots and positions of the requests' new tokens, on the GPU."""
+    d = torch.cuda.current_device()
+    _check("sgq_cache_plan", load().sgq_cache_plan(
+        _dev("lens", lens, _INT32, d), _dev("news", news, _INT32, d), R, page, num_pages,
+        _dev("table", table, _INT32, d), table_ld, _dev("held", held, _INT32, d),
+        _dev("held_out", held_out, _INT32, d), _dev("free_pages", free_pages, _INT32, d),
+        _dev("free_count", free_count, _INT32, d),
+        _dev("free_count_out", free_count_out, _INT32, d), _dev("depth", depth, _INT32, d),
+        max_tokens, _dev("cu_new", cu_new, _INT32, d), _dev("slots", slots, _INT64, d),
+        _dev("pos", pos, _INT32, d), _dev("req", req, _INT32, d),
+        _dev("status", status, _INT32, d), _stream(stream)))
+
+
+def sgq_cache_write(q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_len, slots,
+                    q_out, ld_qo, cache, status=None, stream=None):
+    """Rotate q and k by position; q to q_out, k and v into their slots of ``cache`` (a Cache)."""
+    d = torch.cuda.current_device()
+    _check("sgq_cache_write", load().sgq_cache_write(
+        _dev("q", q, _BF16, d), ld_q, _dev("k", k, _BF16, d), ld_k, _dev("v", v, _BF16, d), ld_v,
+        T, _dev("n_tokens", n_tokens, _INT32, d), Hq, _dev("pos", pos, _INT32, d),
+        _dev("rope", rope, _FLOAT32, d), rope_len, _dev("slots", slots, _INT64, d),
+        _dev("q_out", q_out, _BF16, d), ld_qo, cache.on(d), _dev("status", status, _INT32, d),
+        _stream(stream)))
+
+
+def sgq_tree_attn_workspace_bytes(T: int, R: int, Hq: int, Hkv: int, D: int) -> int:
+    return load().sgq_tree_attn_workspace_bytes(T, R, Hq, Hkv, D)
+
+
+def sgq_tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
+                  scale, out, ld_out, lse, workspace, status=None, stream=None):
+    """Attention of each request's new tokens over its pages of ``cache`` (a Cache)."""
+    d = torch.cuda.current_device()
+    _check("sgq_tree_attn", load().sgq_tree_attn(
+        _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _INT32, d),
+        _dev("cu_new", cu_new, _INT32, d), _dev("table", table, _INT32, d), table_ld,
+        cache.on(d), _dev("tree", tree, _WORDS, d), tree_words, float(scale),
+        _dev("out", out, _BF16, d), ld_out, _dev("lse", lse, _FLOAT32, d),
+        _dev("workspace", workspace, _INT32, d), workspace.numel() * 4,
+        _dev("status", status, _INT32, d), _stream(stream)))
+
+
+def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_out, ld_ro,
+                      w_pre, w_offset, x, ld_x, B, H, eps, stream=None):
+    """The norms around a block with its gate and scaled residual; the element
+    types of the C entry point (a_type, r_type, w_type) are the tensors' own."""
+    d = torch.cuda.current_device()
+    w_types = {t.dtype for t in (w_post, gate, w_pre) if t is not None}
+    if len(w_types) > 1 or (resid_out is not None and resid_out.dtype != resid.dtype):
+        raise TypeError("sgq_residual_norm: w_post, gate and w_pre share one element type, "
+                        "as do resid and resid_out")
+    _check("sgq_residual_norm", load().sgq_residual_norm(
+        _dev("a", a, _FLOATS, d), ld_a, _FLOATS[a.dtype] if a is not None else SGQ_TYPE_F32,
+        _dev("w_post", w_post, _FLOATS, d), _dev("gate", gate, _FLOATS, d), ld_gate,
+        float(scale), _dev("resid", resid, _FLOATS, d), ld_r, _FLOATS[resid.dtype],
+        _dev("resid_out", resid_out, _FLOATS, d), ld_ro, _dev("w_pre", w_pre, _FLOATS, d),
+        _FLOATS[w_types.pop()] if w_types else SGQ_TYPE_F32, float(w_offset),
+        _dev("x", x, _BF16, d), ld_x, B, H, float(eps), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
 # Allocation helpers (torch device memory; plumbing only).
 # --------------------------------------------------------------------------
 
@@ -358,3 +496,8 @@ def alloc_mask(K, device="cuda"):
 def alloc_select(K, device="cuda"):
     return (torch.empty(K, dtype=torch.int32, device=device),
             torch.zeros(1, dtype=torch.int32, device=device))
+
+
+def alloc_tree_attn_workspace(T, R, Hq, Hkv, D, device="cuda"):
+    return torch.empty(sgq_tree_attn_workspace_bytes(T, R, Hq, Hkv, D) // 4, dtype=torch.int32,
+                       device=device)

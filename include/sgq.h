@@ -58,12 +58,14 @@ extern "C" {
 #define SGQ_ERR_CUDA       -8  /* a CUDA runtime call or launch failed           */
 #define SGQ_ERR_DEVICE     -9  /* current device is not compute capability 10.x  */
 #define SGQ_ERR_TOO_LARGE -10  /* N above SGQ_NOALLOC_MAX_N (no-allocation entry)  */
+#define SGQ_ERR_TYPE      -11  /* unknown element type, or one not taken here      */
 
 /* Device status bits (OR-ed into the optional `status` word). */
 #define SGQ_STATUS_NONFINITE_W  1  /* sgq_pack: W holds NaN or Inf (that group packed as zeros) */
-#define SGQ_STATUS_BAD_INDEX    2  /* sgq_gemv: an index outside [0, K) was skipped             */
-#define SGQ_STATUS_BAD_COUNT    4  /* sgq_gemv: *count outside [0, K]; clamped                  */
+#define SGQ_STATUS_BAD_INDEX    2  /* an index (channel, page, slot, position) out of range was skipped */
+#define SGQ_STATUS_BAD_COUNT    4  /* a device-held count or length out of range was clamped    */
 #define SGQ_STATUS_TIMEOUT      8  /* a bounded wait inside a GEMV kernel ran out: y is not valid */
+#define SGQ_STATUS_NO_PAGES    16  /* sgq_cache_plan: the free list does not hold enough pages  */
 /* After SGQ_STATUS_TIMEOUT the tensor-core kernel may have freed its tensor
  * memory with MMAs still in flight: treat it as fatal for the results of that
  * context until the stream has drained. */
@@ -71,6 +73,11 @@ extern "C" {
 /* Activations for sgq_glu. */
 #define SGQ_ACT_SILU 0
 #define SGQ_ACT_RELU 1
+
+/* Element types of the step entry points (sgq_residual_norm, sgq_cache). */
+#define SGQ_TYPE_BF16 0
+#define SGQ_TYPE_F32  1
+#define SGQ_TYPE_E4M3 2  /* 8-bit float, 4 exponent and 3 mantissa bits, no infinities */
 
 /*
  * Sizes of the packed buffers for an N x K weight with the given group size.
@@ -369,6 +376,163 @@ int sgq_ffn(const void *qweight_gu, const void *sz_gu, const void *qweight_d, co
 int sgq_gemv_thresh_noalloc(const void *qweight, const void *sz, int N, int K, int group,
                             const void *x, float t, void *y, float *y_f32, int32_t *status,
                             void *stream);
+
+/*
+ * The step around the projections: a paged key/value cache, attention of a
+ * step's new tokens over it, and the norms around a block. The pages these
+ * kernels' GEMVs come from say nothing of them; they are what a decode or
+ * verification step of 1..16 rows (and wider ones) needs next to its GEMVs.
+ *
+ * A cache is num_pages pages of `page` slots; a slot holds one token's keys
+ * (values) of every kv head, `dim` elements each. Element e of (page g, slot s
+ * of it, head h) is at g page_stride + s slot_stride + h head_stride + e, in
+ * elements, so both slot-major and head-major pages are described. A slot's
+ * number over the whole cache is g * page + s.
+ */
+#define SGQ_MAX_REQUESTS 8192
+typedef struct sgq_cache {
+    void *k, *v;       /* device; same type and strides                              */
+    int type;          /* SGQ_TYPE_BF16, or SGQ_TYPE_E4M3: key = k_scale * stored    */
+    int page;          /* slots of a page, 1..2^20 (any number, not only powers of 2) */
+    int num_pages;
+    int heads;         /* kv heads                                                    */
+    int dim;           /* 64 or 128                                                   */
+    long long page_stride, slot_stride, head_stride; /* elements; multiples of 16 bytes,
+                          and at least dim where there is more than one             */
+    float k_scale, v_scale; /* 1 for SGQ_TYPE_BF16, finite and > 0 for SGQ_TYPE_E4M3 */
+} sgq_cache;
+
+/*
+ * Block tables and slot maps from the requests' lengths, on the GPU.
+ *
+ *   lens, news  int32 [R]: tokens of request r in the cache, and new ones now
+ *               (0 allowed). 1 <= R <= SGQ_MAX_REQUESTS.
+ *   table       int32 [R][table_ld]: row r's first held[r] entries are its
+ *               pages; new pages are written behind them. No other entry is
+ *               touched. table_ld * page <= 2^30.
+ *   held        int32 [R]: pages in each row. A row may hold more than its
+ *               tokens need (drafted tokens that were dropped): they are used
+ *               first. held_out: int32 [R], may be held.
+ *   free_pages  int32 [num_pages]: the first *free_count entries are free;
+ *               pages are taken from the end. free_count_out may be free_count.
+ *   depth       optional int32 [tokens]: a drafted token's depth in its tree.
+ *   cu_new      int32 [R + 1]: first row of each request's new tokens.
+ *   slots       int64 [max_tokens]: slot of each new token, in its request's
+ *               order behind the cached ones; -1 where there is none.
+ *   pos, req    optional int32 [max_tokens]: lens + depth (lens + index without
+ *               depth), and the token's request.
+ * Rows at and behind cu_new[R] of slots, pos and req are left as they were.
+ *
+ * Requests are served in order while the free list lasts: a request that needs
+ * a new page gets all its pages if they and those of every request before it
+ * fit, else none, its slots are -1 and SGQ_STATUS_NO_PAGES is set; one that
+ * needs none is always served. SGQ_STATUS_BAD_COUNT: a negative length or
+ * count, or fewer pages held than lens needs (no new tokens are planned for
+ * that request); more new tokens than max_tokens in all (the rows behind are
+ * dropped and cu_new stops at max_tokens); a request longer than a table row
+ * (its slots are -1); *free_count outside [0, num_pages] (clamped).
+ * SGQ_STATUS_BAD_INDEX: a page outside [0, num_pages) (slot -1).
+ * Run again on its own result it gives the same rows. Returns SGQ_ERR_BATCH
+ * for R, SGQ_ERR_SHAPE for the other sizes (max_tokens <= 2^30).
+ */
+int sgq_cache_plan(const int32_t *lens, const int32_t *news, int R, int page, int num_pages,
+                   int32_t *table, int table_ld, const int32_t *held, int32_t *held_out,
+                   const int32_t *free_pages, const int32_t *free_count,
+                   int32_t *free_count_out, const int32_t *depth, int max_tokens,
+                   int32_t *cu_new, int64_t *slots, int32_t *pos, int32_t *req,
+                   int32_t *status, void *stream);
+
+/*
+ * Store a step's keys and values in their slots, with the rotation of q and k
+ * by position (halves paired: elements i and i + dim/2 of a head).
+ *
+ *   q, k, v   bf16 rows of T tokens, ld_* elements apart (e.g. the three parts
+ *             of one stacked projection's output). q may be NULL (then Hq and
+ *             q_out are not used).
+ *   n_tokens  optional int32 device scalar (e.g. cu_new + R): rows behind it
+ *             are neither read nor written. Outside [0, T]: clamped, flagged
+ *             SGQ_STATUS_BAD_COUNT.
+ *   rope      optional fp32 [rope_len][dim]: cos of the dim/2 angles of a
+ *             position, then sin. NULL: q and k are stored as they are.
+ *   pos       int32 [T], needed with rope. A position outside [0, rope_len):
+ *             the token is skipped, SGQ_STATUS_BAD_INDEX.
+ *   slots     int64 [T]: -1 skips k and v of the token; any other slot outside
+ *             the cache does too and sets SGQ_STATUS_BAD_INDEX. Slots of one
+ *             call must differ from one another.
+ *   q_out     bf16 rows, ld_qo apart; may be q itself (with ld_qo == ld_q).
+ * Each product and sum of the rotation is rounded to fp32 by itself and the
+ * result once to the stored type (round to nearest even); an SGQ_TYPE_E4M3
+ * cache stores value / scale, saturated at 448, NaN kept.
+ */
+int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k, const void *v,
+                    long long ld_v, int T, const int32_t *n_tokens, int Hq, const int32_t *pos,
+                    const float *rope, int rope_len, const int64_t *slots, void *q_out,
+                    long long ld_qo, const sgq_cache *cache_host, int32_t *status,
+                    void *stream);
+
+/*
+ * Attention of each request's new tokens over its pages: one token, a chain,
+ * or a tree of drafted tokens whose keys and values are in the cache already.
+ *
+ *   s_j = scale * q.k_j over the keys that the token sees,
+ *   out = sum_j softmax(s)_j v_j,   lse = ln sum_j e^(s_j)
+ *
+ *   q         bf16 [T][Hq][dim], rows ld_q apart; query head h uses kv head
+ *             h / (Hq / heads), Hq a multiple of heads.
+ *   lens      int32 [R]: tokens cached before the new ones; new token i of
+ *             request r is key lens[r] + i. table as in sgq_cache_plan.
+ *   cu_new    int32 [R + 1], non-decreasing, cu_new[0] >= 0: rows of request r.
+ *   tree      optional uint32 [T][tree_words]: bit j % 32 of word j / 32 of a
+ *             token's words says that it sees new token j of its own request
+ *             (normally itself and its ancestors); tokens past 32 * tree_words
+ *             are seen by none. NULL: itself and those before it. Every token
+ *             sees all lens[r] cached ones.
+ *   out       bf16 [T][Hq][dim], rows ld_out apart. lse: optional fp32 [T][Hq].
+ *   workspace sgq_tree_attn_workspace_bytes bytes, any content; it holds
+ *             nothing between calls. Calls that may overlap must not share one.
+ * A token that sees no key has out = 0 and lse = -infinity. A key that a token
+ * does not see does not touch its output, whatever the slot holds (NaN too).
+ * Rows of no request are left as they were. A page outside [0, num_pages) is
+ * skipped, its keys unseen, and sets SGQ_STATUS_BAD_INDEX; lengths and rows
+ * outside the buffers' sizes are clamped and set SGQ_STATUS_BAD_COUNT.
+ * Scores, maxima, sums and accumulators are fp32; the weights are rounded to
+ * bf16 (fp16 with an SGQ_TYPE_E4M3 cache) for their product with the values.
+ * Any T, lengths and shares of Hq / heads; table_ld * page <= 2^30. The grid
+ * depends on the arguments alone and nothing is read back: a call can be
+ * captured and replayed on other lengths.
+ */
+size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D);
+int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,
+                  const int32_t *cu_new, const int32_t *table, int table_ld,
+                  const sgq_cache *cache_host, const uint32_t *tree, int tree_words,
+                  float scale, void *out, long long ld_out, float *lse, void *workspace,
+                  size_t ws_bytes, int32_t *status, void *stream);
+
+/*
+ * The norms before and after a block, fused with its gate and its scaled
+ * addition to the residual, over B rows of H channels:
+ *
+ *   u          = a, or a * rsqrt(mean(a^2) + eps) * (w_offset + w_post)
+ *   resid_out  = resid + scale * gate * u
+ *   x          = resid_out * rsqrt(mean(resid_out^2) + eps) * (w_offset + w_pre)
+ *
+ *   a          the block's result (e.g. a GEMV's y or y_f32), SGQ_TYPE_BF16 or
+ *              _F32; NULL: x is the norm of resid alone (the first norm) and
+ *              resid_out is not written.
+ *   w_post     [H], optional: the norm behind the block.
+ *   gate       optional, [H] (ld_gate = 0) or [B][H] (rows ld_gate apart).
+ *   resid_out  may be resid (with ld_ro == ld_r). Same type as resid.
+ *   w_pre, x   the norm before the next block and its bf16 input; x NULL:
+ *              neither is used.
+ *   w_type     of w_post, gate and w_pre. w_offset: 1 for weights stored less one.
+ * fp32 throughout; resid_out and x are each rounded once, x from the unrounded
+ * sum. H a multiple of 8 up to 32768, rows on 16 bytes.
+ */
+int sgq_residual_norm(const void *a, long long ld_a, int a_type, const void *w_post,
+                      const void *gate, long long ld_gate, float scale, const void *resid,
+                      long long ld_r, int r_type, void *resid_out, long long ld_ro,
+                      const void *w_pre, int w_type, float w_offset, void *x, long long ld_x,
+                      int B, int H, float eps, void *stream);
 
 /*
  * Read the device status word (the SGQ_STATUS_* bits that calls OR into it):
