@@ -9,673 +9,731 @@
 // request's new tokens, are the rows of one matrix product: a tile of MT rows
 // reads each key and value once for all of them.
 //
-// Work is cut into units of (request, key head, row tile, 64 keys) in that
-// order, and every CTA takes an equal run of them, whatever the requests'
-// lengths are (they are known on the device only). A run that starts or ends
-// inside a (request, key head, row tile) leaves its unnormalised sums with
-// their maximum and sum in the workspace, and combine_kernel joins them in
-// order; a whole one is written out directly.
-#include "sgq_device.cuh"
-#include "sgq_launch.h"
+// Work is cut into units of 64 keys of one item = (request, key head, row
+// tile), and every CTA (one per SM) takes an equal run of them, whatever the
+// requests' lengths are (they are known on the device only). An item also
+// costs kItemCost units of its own, so that a run of many short requests is
+// no longer than one of a few long ones. A run that starts or ends inside an
+// item leaves its unnormalised sums with their reference and sum in the
+// workspace, and combine_kernel joins them in order; a whole item is written
+// out directly.
+//
+// Both products are tcgen05.mma of 128 rows and 128 keys:
+//  * one warp looks up the pages and copies keys and values by the box
+//    (cp.async.bulk.tensor, 128-byte swizzle), two ring slots per 128 keys;
+//    what lies behind a segment's keys, and bad pages, is filled with zeros by
+//    a box outside the map;
+//  * one thread issues S = Q K^T (both from shared memory) into one of two
+//    accumulators, and O += P V with P read from tensor memory, where it takes
+//    S's place;
+//  * four warps, one accumulator row per thread, turn S into P. Their reference
+//    for the exponent moves only when a row's maximum outgrows it by 2^8, so
+//    O is rescaled rarely;
+//  * a tile of 32 or 64 rows (MT) is laid into the 128 several times, and copy
+//    c takes part c of the keys, its P zero elsewhere: the copies' O are
+//    partial sums over the keys, joined at the segment's end. All four warps
+//    then share the exponentials of a few rows;
+//  * 8-bit keys and values are made fp16 (exact) by four more warps on their
+//    way to the slots the products read.
+//
+// Every wait on a barrier is bounded by 0.2 s; one that runs out sets
+// SGQ_STATUS_TIMEOUT, the thread waits on nothing more and the kernel runs to
+// its end.
 #include "step_launch.cuh"
+#include "tc_device.cuh"
+#include "tree_attn.cuh"
 
 #include <algorithm>
-#include <cuda_fp8.h>
 
 namespace sgq {
 
 namespace {
 
-constexpr int kBN = 64;        // keys per unit
-constexpr int kThreads = 128;
-constexpr int kMaxGrid = 296;  // two CTAs on each of 148 SMs
-constexpr int kMaxMT = 64;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-// Requests, as clamped into the ranges the pointers are known to cover.
-struct Request {
-    int tok, n;    // first row of q, new tokens
-    int len, keys; // cached tokens, len + n
-    int row_tiles;
-    int tiles;     // units per (key head, row tile)
-};
-
-__device__ __forceinline__ Request request_of(const AttnProblem &p, int r, int G, int MT, int &bits)
-{
-    Request q;
-    const int c0 = p.cu_new[r], c1 = p.cu_new[r + 1];
-    q.tok = min(max(c0, 0), p.T);
-    q.n = min(max(c1, q.tok), p.T) - q.tok;
-    int len = p.lens[r];
-    const long long cap = (long long)p.table_ld * p.cache.page;
-    if (c0 != q.tok || c1 != q.tok + q.n || len < 0 || (long long)len + q.n > cap)
-        bits |= SGQ_STATUS_BAD_COUNT;
-    len = (int)min((long long)max(len, 0), max(0ll, cap - q.n));
-    q.len = len;
-    q.keys = (int)min((long long)len + q.n, cap);
-    q.row_tiles = (int)(((long long)q.n * G + MT - 1) / MT);
-    q.tiles = q.n ? (q.keys + kBN - 1) / kBN : 0;
-    return q;
-}
-
-__device__ __forceinline__ long long units_of(const Request &q, int Hkv)
-{
-    return (long long)Hkv * q.row_tiles * q.tiles;
-}
-
-// First unit of CTA c of C, and the CTA that holds unit u.
-__device__ __forceinline__ long long first_unit(long long U, int c, int C) { return U * c / C; }
-__device__ __forceinline__ int cta_of(long long U, long long u, int C)
-{
-    return (int)(((u + 1) * C - 1) / U);
-}
-
-__host__ __device__ inline size_t units_bytes(int R) { return ((size_t)(R + 1) * 8 + 255) / 256 * 256; }
-
-// ---- instructions ----
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool take)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-                 "r"(take ? 16 : 0)
-                 : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-// D += A B on 16 x 8 x 16 with fp32 sums; 8-bit keys and values are exact in
-// fp16, so they and q (scaled, see load_q) and the weights are fp16 there.
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if constexpr (F16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two e4m3 values (bits 0..15) as two fp16 in order; exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v)
-{
-    uint32_t d;
-    asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(d) : "r"(v));
-    return d;
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
+constexpr int kTile = 128; // keys per product
+constexpr int kSoftWarps = 4, kSoftThreads = 32 * kSoftWarps;
+constexpr int kProducer = 4, kIssuer = 5, kConvert = 6; // warps
+constexpr uint32_t kColO = 256;                         // tensor-memory columns: S0, S1, O
+constexpr float kGrowth = 8.0f;                         // binary orders a row's maximum may outgrow its reference
 
 template <int D_, int KV, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_;
     static constexpr bool F8 = KV == SGQ_TYPE_E4M3;
-    static constexpr int ES = F8 ? 1 : 2;
-    static constexpr int ROWB = D * ES;               // bytes of one key
-    static constexpr int CPR = ROWB / 16;             // 16-byte chunks of one key
-    static constexpr int HALF = kBN * ROWB;           // keys (or values) of a stage
-    static constexpr int STAGE = 2 * HALF;
-    static constexpr int NST = STAGE >= 32768 ? 3 : STAGE >= 16384 ? 5 : 8;
-    static constexpr int NR = NST + 1;                // ring of row offsets
-    static constexpr int WM = MT / 16, WN = 4 / WM;   // warps along rows and along keys
-    static constexpr int KW = kBN / WN;               // keys per warp and unit
-    static constexpr int NT = KW / 8;                 // score tiles of 8 keys
-    static constexpr int KS = D / 16;                 // products' steps along the head
-    static constexpr int DT = D / 8;                  // output tiles of 8 columns
-    static constexpr int SMEM = NST * STAGE + NR * kBN * 8 + NR * 8;
-    static_assert(WN * MT * D * 4 <= NST * STAGE, "the warps' sums fit the stages");
+    static constexpr int THREADS = F8 ? 320 : 192;
+    static constexpr int COPIES = 128 / MT, KW = kTile / COPIES; // copies of the rows, keys of each
+    static constexpr int SUB = kTile * 128;                      // 128 rows x 64 elements, swizzled
+    static constexpr int NSUB = D / 64;
+    static constexpr int SLOT = NSUB * SUB;                      // 128 keys (or values), 16 bits
+    static constexpr int RAW = kTile * 128;                      // the same, 8 bits (see TcArgs::pitch)
+    static constexpr int NS = F8 ? 4 : D == 128 ? 6 : 12;
+    static constexpr int RS = F8 ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int Q = SLOT;
+    static constexpr int BARS = 2 * NS + 2 * RS + 8;
+    static constexpr int SMEM = 1024 + Q + NS * SLOT + RS * RAW + BARS * 8;
+    static constexpr int LOADS = F8 ? RS : NS; // slots the copies go to
+    static_assert(SMEM <= 227 * 1024 - 1800, "room for the static arrays");
 };
 
-// Byte offset of 16-byte chunk c of key row r within a half stage. Eight
-// consecutive rows at one chunk fall into eight different 16-byte bank groups
-// (ldmatrix); with 8-bit keys so do two rows' aligned runs of four chunks.
-template <class C>
-__device__ __forceinline__ uint32_t chunk_off(int r, int c)
-{
-    int x;
-    if constexpr (C::ROWB == 64)
-        x = (r >> 1) & 3;
-    else if constexpr (C::F8)
-        x = ((r & 1) << 2) | ((r >> 1) & 3);
-    else
-        x = r & 7;
-    return (uint32_t)(r * C::ROWB + ((c ^ x) << 4));
-}
+struct TcArgs {
+    AttnProblem p;
+    int box;   // rows of a copy's box: the largest power of two up to 64 that divides the page
+    int pitch; // bytes from row to row of an 8-bit slot: a box starts on 128 bytes, so a box
+               // of one 64-byte row leaves the other 64 empty
+};
 
-// The 64 keys from kb0 on that a token sees, bit by key: all of the context,
-// and of the drafted tokens those its tree words name (no tree: itself and the
-// ones before it).
-__device__ __forceinline__ uint64_t visible(const AttnProblem &p, const Request &q, int i, int kb0)
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+
+// Byte offset of 16-byte chunk c (8 elements) of row r of an operand.
+__device__ __forceinline__ uint32_t op_off(int r, int c)
 {
-    const int start = kb0 - q.len;
-    const int s = max(start, 0);
-    uint64_t d = 0;
-    if (p.tree) {
-        const uint32_t *w = p.tree + (long long)(q.tok + i) * p.tree_words;
-        const int k = s >> 5, sh = s & 31;
-        const uint64_t w0 = k < p.tree_words ? w[k] : 0u;
-        const uint64_t w1 = k + 1 < p.tree_words ? w[k + 1] : 0u;
-        const uint64_t w2 = k + 2 < p.tree_words ? w[k + 2] : 0u;
-        d = (w0 | (w1 << 32)) >> sh;
-        if (sh)
-            d |= w2 << (64 - sh);
-    } else {
-        const int ones = i + 1 - s;
-        d = ones >= 64 ? ~0ull : ones > 0 ? (1ull << ones) - 1 : 0ull;
-    }
-    if (start < 0) {
-        const int sh = -start;
-        d = sh >= 64 ? ~0ull : (d << sh) | ((1ull << sh) - 1);
-    }
-    const int left = q.keys - kb0;
-    return left >= 64 ? d : left > 0 ? d & ((1ull << left) - 1) : 0ull;
+    return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 template <int D, int KV, int MT>
-__global__ void __launch_bounds__(kThreads, 2) attn_kernel(const AttnProblem p)
+__global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
+    attn_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap)
 {
     using C = Cfg<D, KV, MT>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long s_scan[4];
+    const AttnProblem &p = a.p;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ long long s_scan[4], s_first;
     __shared__ int s_r;
-    __shared__ long long s_first;
-    __shared__ float s_m[4][MT], s_l[4][MT];
-    long long *ring = reinterpret_cast<long long *>(smem + C::NST * C::STAGE); // [NR][64], -1: no key
-    uint32_t *bad = reinterpret_cast<uint32_t *>(ring + C::NR * kBN);          // [NR][2]
+    __shared__ float s_m[C::COPIES][MT], s_l[C::COPIES][MT], s_f[MT];
+    __shared__ uint32_t s_bad[8][4]; // keys without a page of the last tiles, bit by key
+    __shared__ uint32_t s_odd[4];    // values that are not finite, bit by key
+    __shared__ int s_acc[2];         // the first product of a segment adds to O
+    uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    const uint32_t sQ = smem_u32(smem), sKV = sQ + C::Q, sRaw = sKV + C::NS * C::SLOT;
+    const uint32_t bars = sRaw + C::RS * C::RAW;
+    const uint32_t bFull = bars, bEmpty = bFull + 8 * C::NS, bRFull = bEmpty + 8 * C::NS, bREmpty = bRFull + 8 * C::RS;
+    const uint32_t bS = bREmpty + 8 * C::RS, bP = bS + 16, bO = bP + 16, bQ = bO + 16, bDone = bQ + 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wm = warp / C::WN, wn = warp % C::WN;
-    const int qd = lane & 3, gr = lane >> 2;
     const int Hkv = p.cache.heads, G = p.Hq / Hkv;
-    const uint32_t sm0 = smem_u32(smem);
-    int bits = 0;
+
+    if (warp == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < C::NS; ++s) {
+            bar_init(bFull + 8 * s, C::F8 ? 4 : 1);
+            bar_init(bEmpty + 8 * s, 1);
+        }
+        for (int s = 0; s < C::RS; ++s) {
+            bar_init(bRFull + 8 * s, 1);
+            bar_init(bREmpty + 8 * s, 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(bS + 8 * b, 1);
+            bar_init(bP + 8 * b, kSoftWarps);
+            bar_init(bO + 8 * b, 1);
+            s_acc[b] = 0;
+        }
+        bar_init(bQ, 1);
+        bar_init(bDone, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_r = p.R;
+    }
     grid_launch_dependents();
     grid_dependency_wait();
 
-    // Units before each request; this CTA's run [u, u_end).
+    // Cost before each request; this CTA's run.
     long long *ws_units = static_cast<long long *>(p.workspace);
     float *ws_part = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + units_bytes(p.R));
-    const int per = (p.R + kThreads - 1) / kThreads;
+    int bits = 0;
+    bool ok = true;
+    const int per = (p.R + kSoftThreads - 1) / kSoftThreads;
     const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r)
-        mine += units_of(request_of(p, r, G, MT, bits), Hkv);
-    long long inc = mine;
+    long long mine = 0, at = 0;
+    if (warp < kSoftWarps) {
+        for (int r = r0; r < r1; ++r)
+            mine += cost_of(request_of(p, r, G, MT, bits), Hkv);
+        long long inc = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o)
-            inc += t;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o)
+                inc += t;
+        }
+        if (lane == 31)
+            s_scan[warp] = inc;
+        at = inc - mine;
     }
-    if (lane == 31)
-        s_scan[warp] = inc;
-    if (tid == 0)
-        s_r = p.R;
+    tc_before();
     __syncthreads();
-    long long U = 0, at = inc - mine;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        at += w < warp ? s_scan[w] : 0;
-        U += s_scan[w];
-    }
-    long long u = first_unit(U, blockIdx.x, gridDim.x);
-    const long long u_end = first_unit(U, blockIdx.x + 1, gridDim.x);
-    if (blockIdx.x == 0 || (u >= at && u < at + mine)) {
-        long long s = at;
-        for (int r = r0; r < r1; ++r) {
-            const long long n = units_of(request_of(p, r, G, MT, bits), Hkv);
-            if (u >= s && u < s + n) {
-                s_r = r;
-                s_first = s;
+    tc_after();
+    const uint32_t tmem = s_tmem;
+    const long long U = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+    Walk walk;
+    walk.u = run_start(U, blockIdx.x, gridDim.x);
+    walk.u_end = run_start(U, blockIdx.x + 1, gridDim.x);
+    if (warp < kSoftWarps) {
+        for (int w = 0; w < warp; ++w)
+            at += s_scan[w];
+        if (blockIdx.x == 0 || (walk.u >= at && walk.u < at + mine)) {
+            long long s = at;
+            int none = 0;
+            for (int r = r0; r < r1; ++r) {
+                const long long n = cost_of(request_of(p, r, G, MT, none), Hkv);
+                if (walk.u >= s && walk.u < s + n) {
+                    s_r = r;
+                    s_first = s;
+                }
+                if (blockIdx.x == 0)
+                    ws_units[r] = s;
+                s += n;
             }
-            if (blockIdx.x == 0)
-                ws_units[r] = s;
-            s += n;
+            if (blockIdx.x == 0 && r1 == p.R)
+                ws_units[p.R] = U;
         }
-        if (blockIdx.x == 0 && r1 == p.R)
-            ws_units[p.R] = U;
+        if (bits && blockIdx.x == 0)
+            set_status(p.status, bits);
     }
-    if (bits && blockIdx.x == 0)
-        set_status(p.status, bits);
     __syncthreads();
-    int r = s_r;
-    if (u >= u_end || r >= p.R)
-        return;
-    long long base = s_first;
-    Request rq = request_of(p, r, G, MT, bits);
-    bits = 0;
+    walk.r = s_r;
+    walk.base = s_first;
+    if (walk.r >= p.R)
+        walk.u_end = walk.u; // nothing to do
+    else {
+        int none = 0;
+        walk.rq = request_of(p, walk.r, G, MT, none);
+    }
 
-    while (u < u_end) {
-        while (u >= base + units_of(rq, Hkv)) {
-            base += units_of(rq, Hkv);
-            rq = request_of(p, ++r, G, MT, bits);
-        }
-        const long long in_r = u - base;
-        const long long item = in_r / rq.tiles;
-        const int j0 = (int)(in_r - item * rq.tiles);
-        const int nt = (int)min((long long)(rq.tiles - j0), u_end - u);
-        const int h = (int)(item / rq.row_tiles), rt = (int)(item - (long long)h * rq.row_tiles);
-        const int32_t *table = p.table + (long long)r * p.table_ld;
-
-        // Element offset of key `key`'s row for this head, or -1.
-        auto page_id = [&](int key) -> int {
-            return key < rq.keys ? table[key / p.cache.page] : -1;
-        };
-        auto put_row = [&](int tile, int row, int id) { // whole warps, 32 consecutive rows
-            const int key = (j0 + tile) * kBN + row;
-            const bool want = key < rq.keys, ok = want && id >= 0 && id < p.cache.num_pages;
-            ring[(tile % C::NR) * kBN + row] =
-                ok ? id * p.cache.page_stride + (key % p.cache.page) * p.cache.slot_stride : -1;
-            const uint32_t b = __ballot_sync(~0u, want && !ok);
-            if ((row & 31) == 0)
-                bad[(tile % C::NR) * 2 + (row >> 5)] = b;
-            if (b && (row & 31) == 0)
-                set_status(p.status, SGQ_STATUS_BAD_INDEX);
-        };
-        auto issue = [&](int tile) {
-            const uint32_t st = sm0 + (uint32_t)(tile % C::NST) * C::STAGE;
-            const long long *off = ring + (tile % C::NR) * kBN;
-            const uint8_t *kh = static_cast<const uint8_t *>(p.cache.k) + h * p.cache.head_stride * C::ES;
-            const uint8_t *vh = static_cast<const uint8_t *>(p.cache.v) + h * p.cache.head_stride * C::ES;
+    if (warp == kProducer) {
+        // ---- pages -> slots ----------------------------------------------
+        const uint32_t full = C::F8 ? bRFull : bFull, empty = C::F8 ? bREmpty : bEmpty;
+        const uint32_t dst0 = C::F8 ? sRaw : sKV;
+        const uint32_t bytes = C::F8 ? kTile * D : C::SLOT; // of one slot's boxes
+        constexpr uint32_t STEP = C::F8 ? C::RAW : C::SLOT;
+        const int row_bytes = C::F8 ? a.pitch : 128;
+        constexpr int PARTS = C::F8 ? 1 : C::NSUB; // boxes side by side in a row
+        const int boxes = kTile / a.box;
+        const int page = p.cache.page;
+        int i = 0, issued = 0; // tiles, slots so far
+        while (walk.next(p, G, MT)) {
+            const int32_t *table = p.table + (long long)walk.r * p.table_ld;
+            const int key0 = walk.j0 * kBN, end = walk.key_end();
+            const int nt = (walk.nu + 1) / 2;
+            // the pages of a tile's boxes: box lane + 32 j of the tile in id[j]
+            int id[4];
+            auto look = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < kBN * C::CPR / kThreads; ++i) {
-                const int idx = tid + i * kThreads, row = idx / C::CPR, c = idx % C::CPR;
-                const long long o = off[row];
-                const bool take = o >= 0;
-                const long long e = take ? o * C::ES + c * 16 : 0;
-                const uint32_t d = st + chunk_off<C>(row, c);
-                cp_async16_zfill(d, kh + e, take);
-                cp_async16_zfill(d + C::HALF, vh + e, take);
-            }
-        };
-
-        // Fill: offsets of the first NST units, loads of the first NST - 1.
-        for (int i = tid; i < C::NST * kBN; i += kThreads) {
-            const int tile = i / kBN, row = i % kBN;
-            put_row(tile, row, page_id((j0 + tile) * kBN + row));
-        }
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < C::NST - 1; ++s) {
-            if (s < nt)
-                issue(s);
-            cp_async_commit();
-        }
-        int next_id = -1;
-        if (tid < kBN)
-            next_id = page_id((j0 + C::NST) * kBN + tid);
-
-        // This thread's two rows: row g of the tile is (token g / G, head g % G).
-        int tok_i[2];
-        bool live[2];
-        const uint16_t *qrow[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int g = rt * MT + wm * 16 + gr + 8 * e;
-            tok_i[e] = g / G;
-            live[e] = tok_i[e] < rq.n;
-            if (!live[e])
-                tok_i[e] = 0;
-            qrow[e] = p.q + (rq.tok + tok_i[e]) * p.ld_q + (long long)(h * G + (live[e] ? g % G : 0)) * D;
-        }
-        // q in the products' A layout. With 8-bit keys a thread's 16 bytes of
-        // a key are four steps' worth, so the head's order inside the steps is
-        // permuted, the same way for q and k; and q becomes fp16, each row by
-        // the power of two that brings its largest value into [2^7, 2^8): exact
-        // for values down to 2^-21 of that, below it off by at most 2^-33 of it.
-        uint32_t qf[C::KS][4];
-        float factor[2] = {p.scale * p.cache.k_scale * kLog2e, p.scale * p.cache.k_scale * kLog2e};
-        if constexpr (!C::F8) {
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    qf[s][e] = live[e] ? *reinterpret_cast<const uint32_t *>(qrow[e] + s * 16 + 2 * qd) : 0u;
-                    qf[s][e + 2] = live[e] ? *reinterpret_cast<const uint32_t *>(qrow[e] + s * 16 + 8 + 2 * qd) : 0u;
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + t * kTile + (lane + 32 * j) * a.box;
+                    id[j] = lane + 32 * j < boxes && key < end ? table[key / page] : -1;
                 }
-        } else {
+            };
+            look(0);
+            for (int t = 0; t < nt; ++t, ++i) {
+                int pid[4], slot[4];
+                bool any = false;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint2 raw[C::KS];
-                float mx = 0.0f;
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) {
-                    raw[s] = live[e] ? *reinterpret_cast<const uint2 *>(qrow[e] + (s >> 2) * 64 + qd * 16 + (s & 3) * 4)
-                                     : make_uint2(0u, 0u);
-                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[s].x << 16)), fabsf(__uint_as_float(raw[s].x & 0xffff0000u))));
-                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[s].y << 16)), fabsf(__uint_as_float(raw[s].y & 0xffff0000u))));
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + t * kTile + (lane + 32 * j) * a.box;
+                    const bool want = lane + 32 * j < boxes && key < end;
+                    const bool good = want && id[j] >= 0 && id[j] < p.cache.num_pages;
+                    pid[j] = good ? id[j] : p.cache.num_pages; // outside the map: zeros
+                    slot[j] = good ? key % page : 0;
+                    any |= want && !good;
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                // exponent of the power of two, kept where both it and its
-                // inverse are normal fp32 numbers
-                const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
-                const int up = min(max(7 - ex, -126), 126);
-                const float mul = pow2f(up);
-                factor[e] *= pow2f(-up);
+                any = __any_sync(~0u, any);
+                if (lane < 4)
+                    s_bad[i & 7][lane] = 0;
+                __syncwarp();
+                if (any) {
 #pragma unroll
-                for (int s = 0; s < C::KS; ++s) {
-                    qf[s][e] = pack2<true>(__uint_as_float(raw[s].x << 16) * mul,
-                                           __uint_as_float(raw[s].x & 0xffff0000u) * mul);
-                    qf[s][e + 2] = pack2<true>(__uint_as_float(raw[s].y << 16) * mul,
-                                               __uint_as_float(raw[s].y & 0xffff0000u) * mul);
-                }
-            }
-        }
-
-        float acc[C::DT][4];
-#pragma unroll
-        for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[d][e] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-        for (int t = 0; t < nt; ++t) {
-            cp_async_wait<C::NST - 2>();
-            __syncthreads();
-            if (t + C::NST - 1 < nt)
-                issue(t + C::NST - 1);
-            cp_async_commit();
-            if (tid < kBN) {
-                put_row(t + C::NST, tid, next_id);
-                next_id = page_id((j0 + t + C::NST + 1) * kBN + tid);
-            }
-            const uint32_t ks = sm0 + (uint32_t)(t % C::NST) * C::STAGE, vs = ks + C::HALF;
-            const int kb0 = (j0 + t) * kBN, kw = wn * C::KW;
-
-            float s[C::NT][4];
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] = 0.0f;
-            if constexpr (!C::F8) {
-#pragma unroll
-                for (int n2 = 0; n2 < C::NT / 2; ++n2)
-#pragma unroll
-                    for (int st = 0; st < C::KS; ++st) {
-                        uint32_t b[4];
-                        ldmatrix4(b, ks + chunk_off<C>(kw + n2 * 16 + ((lane >> 4) << 3) + (lane & 7),
-                                                       st * 2 + ((lane >> 3) & 1)));
-                        mma16816<false>(s[2 * n2], qf[st], b[0], b[1]);
-                        mma16816<false>(s[2 * n2 + 1], qf[st], b[2], b[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = lane + 32 * j, key = key0 + t * kTile + b * a.box;
+                        if (b < boxes && key < end && pid[j] == p.cache.num_pages)
+                            for (int k = 0; k < a.box; ++k)
+                                atomicOr(&s_bad[i & 7][(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
                     }
-            } else {
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                    for (int sg = 0; sg < C::KS / 4; ++sg) {
-                        const uint4 b = *reinterpret_cast<const uint4 *>(
-                            smem + (ks - sm0) + chunk_off<C>(kw + n * 8 + gr, sg * 4 + qd));
-                        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int st = 0; st < 4; ++st)
-                            mma16816<true>(s[n], qf[sg * 4 + st], e4m3x2_to_f16x2(w[st] & 0xffffu),
-                                           e4m3x2_to_f16x2(w[st] >> 16));
-                    }
-            }
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] *= factor[e >> 1];
-
-            // Units that reach the drafted tokens, or hold a key without a page.
-            const uint32_t bad0 = bad[(t % C::NR) * 2], bad1 = bad[(t % C::NR) * 2 + 1];
-            const bool masked = kb0 + kBN > rq.len || (bad0 | bad1);
-            uint64_t vis[2] = {~0ull, ~0ull};
-            bool odd_v = false;
-            if (masked) {
-                const uint64_t good = ~((uint64_t)bad0 | ((uint64_t)bad1 << 32));
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    vis[e] = (visible(p, rq, tok_i[e], kb0) & good) >> kw;
-#pragma unroll
-                    for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (!((vis[e] >> (n * 8 + 2 * qd + c)) & 1))
-                                s[n][2 * e + c] = -INFINITY;
+                    if (lane == 0)
+                        set_status(p.status, SGQ_STATUS_BAD_INDEX);
+                    __syncwarp();
                 }
-                // a value that is not finite must not reach, times zero, the
-                // rows that do not see its key
-                for (int i = tid; i < kBN * C::CPR; i += kThreads) {
-                    const int row = i / C::CPR;
-                    if (kb0 + row >= rq.len) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            smem + (vs - sm0) + chunk_off<C>(row, i % C::CPR));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (t + 1 < nt)
+                    look(t + 1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (C::F8)
-                                odd_v |= __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-                            else
-                                odd_v |= __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u) != 0;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int n = 2 * i + kv, s = n % C::LOADS;
+                    if (n >= C::LOADS)
+                        bar_wait(empty + 8 * s, (n / C::LOADS - 1) & 1, ok);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    issued = n + 1;
+                    if (lane == 0)
+                        bar_expect(full + 8 * s, bytes);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = lane + 32 * j;
+                        if (b < boxes)
+#pragma unroll
+                            for (int c = 0; c < PARTS; ++c)
+                                tma_load_4d(dst0 + s * STEP + c * C::SUB + b * a.box * row_bytes, kv ? &vmap : &kmap,
+                                            c * 64, slot[j], walk.h, pid[j], full + 8 * s);
+                    }
+                }
+            }
+        }
+        // every copy has landed before the CTA ends, whatever went wrong
+        bool landed = true;
+        for (int n = max(0, issued - C::LOADS); n < issued; ++n)
+            bar_wait(full + 8 * (n % C::LOADS), (n / C::LOADS) & 1, landed);
+        ok = ok && landed;
+    } else if (warp == kIssuer) {
+        // ---- the products ------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
+            const uint64_t dq = desc_sw128(sQ, 16, 1024);
+            auto scores = [&](int i) {
+                const int n = 2 * i, s = n % C::NS;
+                bar_wait(bFull + 8 * s, (n / C::NS) & 1, ok);
+                tc_after();
+                const uint64_t dk = desc_sw128(sKV + s * C::SLOT, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t step = (uint64_t)(((k >> 2) * C::SUB + (k & 3) * 32) >> 4);
+                    mma_ss(tmem + (i & 1) * kTile, dq + step, dk + step, idS, k > 0);
+                }
+                tc_commit(bEmpty + 8 * s);
+                tc_commit(bS + 8 * (i & 1));
+            };
+            int i = 0, seg = 0;
+            while (walk.next(p, G, MT)) {
+                const int nt = (walk.nu + 1) / 2;
+                bar_wait(bQ, seg & 1, ok);
+                ++seg;
+                scores(i);
+                for (int t = 0; t < nt; ++t, ++i) {
+                    if (t + 1 < nt)
+                        scores(i + 1);
+                    const int n = 2 * i + 1, s = n % C::NS;
+                    bar_wait(bFull + 8 * s, (n / C::NS) & 1, ok);
+                    bar_wait(bP + 8 * (i & 1), (i >> 1) & 1, ok);
+                    tc_after();
+                    const uint32_t add = t > 0 || *(volatile int *)&s_acc[i & 1];
+                    const uint64_t dv = desc_sw128(sKV + s * C::SLOT, C::SUB, 1024);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + kColO, tmem + (i & 1) * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
+                    tc_commit(bEmpty + 8 * s);
+                    tc_commit(bO + 8 * (i & 1));
+                }
+            }
+            tc_commit(bDone);
+            bool done = true;
+            bar_wait(bDone, 0, done);
+            ok = ok && done;
+        }
+        __syncwarp();
+    } else if (C::F8 && warp >= kConvert) {
+        // ---- 8-bit slots -> fp16 slots -----------------------------------
+        const int ct = tid - 32 * kConvert;
+        int n = 0;
+        while (walk.next(p, G, MT)) {
+            const int last = n + 2 * ((walk.nu + 1) / 2);
+            for (; n < last; ++n) {
+                const int rs = n % max(C::RS, 1), s = n % C::NS;
+                bar_wait(bRFull + 8 * rs, (n / max(C::RS, 1)) & 1, ok);
+                if (n >= C::NS)
+                    bar_wait(bEmpty + 8 * s, (n / C::NS - 1) & 1, ok);
+                __syncwarp();
+                const uint8_t *src = smem + (sRaw - sQ) + rs * C::RAW;
+                uint8_t *dst = smem + (sKV - sQ) + s * C::SLOT;
+#pragma unroll 4
+                for (int k = 0; k < kTile * D / 16 / 128; ++k) {
+                    const int idx = ct + k * 128, row = idx / (D / 16), c = idx % (D / 16);
+                    const int x = c ^ (((row * a.pitch) >> 7) & (D / 16 - 1)); // the copies' swizzle
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + row * a.pitch + 16 * x);
+                    *reinterpret_cast<uint4 *>(dst + op_off(row, 2 * c)) =
+                        make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
+                                   e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
+                    *reinterpret_cast<uint4 *>(dst + op_off(row, 2 * c + 1)) =
+                        make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
+                                   e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16));
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(bFull + 8 * s);
+                    bar_arrive(bREmpty + 8 * rs);
+                }
+            }
+        }
+    } else {
+        // ---- the softmax -------------------------------------------------
+        const int quad = warp / (MT / 32), row = (warp % (MT / 32)) * 32 + lane; // copy, row of the tile
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const uint32_t tO = tmem + kColO + lanes;
+        int i = 0;
+        while (walk.next(p, G, MT)) {
+            const Request &rq = walk.rq;
+            const int nt = (walk.nu + 1) / 2, end = walk.key_end(), key0 = walk.j0 * kBN;
+
+            // Q, once per copy of the rows. With 8-bit keys q becomes fp16, each
+            // row by the power of two that brings its largest value into
+            // [2^7, 2^8): exact for values down to 2^-21 of that, below it off
+            // by at most 2^-33 of it. A negative scale's sign goes to q, so that
+            // the largest score is the largest exponent.
+            {
+                constexpr int CH = D / 8, N = MT * CH / kSoftThreads;
+                uint4 v[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int idx = tid + k * kSoftThreads, g = walk.rt * MT + idx / CH, ti = g / G;
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (ti < rq.n)
+                        v[k] = *reinterpret_cast<const uint4 *>(
+                            p.q + (rq.tok + ti) * p.ld_q + (long long)(walk.h * G + g % G) * D + 8 * (idx % CH));
+                }
+                const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int idx = tid + k * kSoftThreads, qr = idx / CH, c = idx % CH;
+                    uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
+                    if constexpr (C::F8) {
+                        float mx = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+#pragma unroll
+                        for (int o = CH / 2; o; o >>= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                        // both the power and its inverse are normal fp32 numbers
+                        const int up = min(max(7 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
+                        const float mul = pow2f(up);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<true>(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
+                        if (c == 0)
+                            s_f[qr] = pow2f(-up);
+                    }
+#pragma unroll
+                    for (int cp = 0; cp < C::COPIES; ++cp)
+                        *reinterpret_cast<uint4 *>(smem + op_off(qr + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_async_smem();
+                soft_sync();
+                if (tid == 0)
+                    bar_arrive(bQ);
+            }
+            const int g = walk.rt * MT + row;
+            const bool live = g / G < rq.n;
+            const int tok_i = live ? g / G : 0;
+            const bool warp_live = __any_sync(~0u, live);
+            float factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
+            if constexpr (C::F8)
+                factor *= s_f[row];
+            factor = fmaxf(factor, 1e-37f); // a scale of zero: all scores alike
+            float m = -INFINITY, l = 0.0f; // reference (base 2), sum
+
+            for (int t = 0; t < nt; ++t, ++i) {
+                const uint32_t tS = tmem + (i & 1) * kTile + lanes;
+                const int kt = key0 + t * kTile, kq = kt + quad * C::KW; // first key of the tile, of this copy
+                bar_wait(bS + 8 * (i & 1), (i >> 1) & 1, ok);
+                if (i >= 2)
+                    bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, ok);
+                __syncwarp();
+                tc_after();
+                if (tid == 0)
+                    s_acc[i & 1] = 0;
+                uint32_t s[C::KW];
+                if (warp_live) {
+#pragma unroll
+                    for (int c = 0; c < C::KW; c += 32)
+                        tmem_ld32(tS + quad * C::KW + c, s + c);
+#pragma unroll
+                    for (int c = 0; c < C::KW; c += 32)
+                        tmem_ld_wait(s + c);
+                }
+                // Tiles that reach the drafted tokens or the end, or hold a key
+                // without a page.
+                const uint32_t *bad = s_bad[i & 7];
+                if (kt + kTile > min(rq.len, end) || (bad[0] | bad[1] | bad[2] | bad[3])) {
+                    uint64_t vis[(C::KW + 63) / 64];
+#pragma unroll
+                    for (int c = 0; c < C::KW; c += 64) {
+                        const int w = (quad * C::KW + c) >> 5;
+                        const uint64_t b = C::KW >= 64 ? bad[w] | ((uint64_t)bad[w + 1] << 32) : bad[w];
+                        vis[c / 64] = visible(p, rq, tok_i, kq + c, end) & ~b;
+                    }
+#pragma unroll
+                    for (int c = 0; c < C::KW; ++c)
+                        if (!((vis[c / 64] >> (c & 63)) & 1))
+                            s[c] = 0xff800000u;
+                    // Values behind the end become zero; one that is not finite
+                    // must not reach, times zero, the rows that do not see it.
+                    const int n = 2 * i + 1, sl = n % C::NS;
+                    bar_wait(bFull + 8 * sl, (n / C::NS) & 1, ok);
+                    uint8_t *vs = smem + (sKV - sQ) + sl * C::SLOT;
+                    bool odd = false;
+                    if (kt + tid >= end) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4 *>(vs + op_off(tid, c)) = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (kt + tid >= rq.len) {
+                        constexpr uint32_t EXP = C::F8 ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(vs + op_off(tid, c));
+                            odd |= (__vcmpeq2(v.x & EXP, EXP) | __vcmpeq2(v.y & EXP, EXP) | __vcmpeq2(v.z & EXP, EXP) |
+                                    __vcmpeq2(v.w & EXP, EXP)) != 0;
                         }
                     }
-                }
-                odd_v = __syncthreads_or(odd_v);
-            }
-
-            float corr[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = m[e];
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n)
-                    mx = fmaxf(mx, fmaxf(s[n][2 * e], s[n][2 * e + 1]));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                const float ref = mx == -INFINITY ? 0.0f : mx; // nothing seen yet
-                corr[e] = exp2_fast(m[e] - ref);
-                m[e] = mx;
-                float sum = 0.0f;
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        s[n][2 * e + c] = exp2_fast(s[n][2 * e + c] - ref);
-                        sum += s[n][2 * e + c];
-                    }
-                l[e] = l[e] * corr[e] + sum;
-            }
-#pragma unroll
-            for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[d][e] *= corr[e >> 1];
-
-            if (!odd_v) {
-                // The weights are rounded to the values' type for the product
-                // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the small ones, 2^-25);
-                // their sum l is of the unrounded ones.
-#pragma unroll
-                for (int k2 = 0; k2 < C::NT / 2; ++k2) {
-                    const uint32_t a[4] = {pack2<C::F8>(s[2 * k2][0], s[2 * k2][1]),
-                                           pack2<C::F8>(s[2 * k2][2], s[2 * k2][3]),
-                                           pack2<C::F8>(s[2 * k2 + 1][0], s[2 * k2 + 1][1]),
-                                           pack2<C::F8>(s[2 * k2 + 1][2], s[2 * k2 + 1][3])};
-#pragma unroll
-                    for (int d2 = 0; d2 < C::CPR / 2; ++d2) {
-                        uint32_t b[4];
-                        ldmatrix4_trans(b, vs + chunk_off<C>(kw + k2 * 16 + (((lane >> 3) & 1) << 3) + (lane & 7),
-                                                             d2 * 2 + (lane >> 4)));
-                        if constexpr (!C::F8) {
-                            mma16816<false>(acc[2 * d2], a, b[0], b[1]);
-                            mma16816<false>(acc[2 * d2 + 1], a, b[2], b[3]);
-                        } else {
-                            // a transposed 16-bit element is two columns of one
-                            // key: even columns make one product, odd the next
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const uint32_t x = b[2 * c], y = b[2 * c + 1];
-                                mma16816<true>(acc[4 * d2 + 2 * c], a,
-                                               e4m3x2_to_f16x2(__byte_perm(x, 0, 0x4420)),
-                                               e4m3x2_to_f16x2(__byte_perm(y, 0, 0x4420)));
-                                mma16816<true>(acc[4 * d2 + 2 * c + 1], a,
-                                               e4m3x2_to_f16x2(__byte_perm(x, 0, 0x4431)),
-                                               e4m3x2_to_f16x2(__byte_perm(y, 0, 0x4431)));
-                            }
-                        }
-                    }
-                }
-            } else {
-                // Rare: key by key in fp32, each row adding the keys it sees.
-                float w[C::NT][4];
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[n][e] = s[n][e];
+                    __syncwarp();
+                    const uint32_t ob = __ballot_sync(~0u, odd);
+                    if (lane == 0)
+                        s_odd[warp] = ob;
+                    soft_sync();
+                    if (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) {
+                        // Rare: what is not finite is added to O here, for the
+                        // rows that see it, and taken out of the slot.
+                        if (t > 0)
+                            bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, ok);
+                        __syncwarp();
+                        tc_after();
 #pragma unroll 1
-                for (int k = 0; k < C::KW; ++k) {
-                    const int from = (lane & ~3) | ((k & 7) >> 1);
-                    float pk[2];
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c, o);
+                            tmem_ld_wait(o);
+                            if (t == 0)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        pk[e] = __shfl_sync(~0u, w[k >> 3][2 * e + (k & 1)], from);
-                    const uint8_t *row = smem + (vs - sm0);
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = 0u;
+#pragma unroll 1
+                            for (int k = 0; k < C::KW; ++k) {
+                                const int kr = quad * C::KW + k; // row of the slot
+                                if (!((s_odd[kr >> 5] >> (kr & 31)) & 1) || !((vis[k >> 6] >> (k & 63)) & 1))
+                                    continue;
 #pragma unroll
-                    for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float v;
-                            if constexpr (C::F8) {
-                                const int col = 16 * (d >> 1) + 4 * qd + 2 * c + (d & 1);
-                                const uint8_t b = row[chunk_off<C>(kw + k, col >> 4) + (col & 15)];
-                                const uint32_t hv = e4m3x2_to_f16x2(b);
-                                v = __half2float(__ushort_as_half((unsigned short)(hv & 0xffffu)));
-                            } else {
-                                const int col = 8 * d + 2 * qd + c;
-                                v = bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(
-                                    row + chunk_off<C>(kw + k, col >> 3) + 2 * (col & 7)));
+                                for (int e = 0; e < 32; ++e) {
+                                    const uint16_t b = *reinterpret_cast<const uint16_t *>(vs + op_off(kr, (c + e) >> 3) + 2 * (e & 7));
+                                    const float v = C::F8 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
+                                    if (!isfinite(v))
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+                                }
                             }
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if ((vis[e] >> k) & 1)
-                                    acc[d][2 * e + c] = fmaf(pk[e], v, acc[d][2 * e + c]);
+                            __syncwarp();
+                            tmem_st32(tO + c, o);
                         }
+                        tmem_st_wait();
+                        soft_sync();
+                        if (odd) {
+                            constexpr uint16_t EXP = C::F8 ? 0x7c00 : 0x7f80;
+                            for (int e = 0; e < D; ++e) {
+                                uint16_t *b = reinterpret_cast<uint16_t *>(vs + op_off(tid, e >> 3) + 2 * (e & 7));
+                                if ((*b & EXP) == EXP)
+                                    *b = 0;
+                            }
+                        }
+                        if (tid == 0)
+                            s_acc[i & 1] = t == 0;
+                    }
+                    fence_async_smem();
+                    soft_sync();
                 }
+                if (warp_live) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < C::KW; ++c)
+                        mx = fmaxf(mx, __uint_as_float(s[c]));
+                    mx *= factor;
+                    // the reference moves for the first keys seen, and when outgrown
+                    const bool grow = mx > m + kGrowth || (m == -INFINITY && mx > m);
+                    if (__any_sync(~0u, grow)) {
+                        const float to = grow ? mx : m;
+                        const float corr = grow ? exp2_fast(m - to) : 1.0f;
+                        m = to;
+                        l *= corr;
+                        if (t > 0) {
+                            bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, ok);
+                            __syncwarp();
+                            tc_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + c, o);
+                                tmem_ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                                tmem_st32(tO + c, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : m; // nothing seen yet
+                    // The weights are rounded to the values' type for the product
+                    // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
+                    // small ones, 2^-25); their sum l is of the unrounded ones.
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t w[C::KW / 2];
+#pragma unroll
+                    for (int c = 0; c < C::KW; c += 2) {
+                        const float x = exp2_fast(fmaf(__uint_as_float(s[c]), factor, -ref));
+                        const float y = exp2_fast(fmaf(__uint_as_float(s[c + 1]), factor, -ref));
+                        sum[c & 2] += x;
+                        sum[(c & 2) + 1] += y;
+                        w[c / 2] = pack2<C::F8>(x, y);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    if constexpr (C::COPIES == 1) {
+                        tmem_st32(tS, w);
+                        tmem_st32(tS + 32, w + 32);
+                    } else {
+                        const uint32_t z[32] = {};
+#pragma unroll
+                        for (int b = 0; b < C::COPIES; ++b) {
+                            if constexpr (MT == 64)
+                                tmem_st32(tS + 32 * b, b == quad ? w : z);
+                            else
+                                tmem_st16(tS + 16 * b, b == quad ? w : z);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(bP + 8 * (i & 1));
             }
-        }
-        cp_async_wait_all();
-        __syncthreads(); // the stages are free: the warps' sums go there
 
-        // Join the warps that shared the rows, and write.
+            // ---- the segment's end: O is complete ----
+            const int last = i - 1;
+            if (last >= 1)
+                bar_wait(bO + 8 * ((last - 1) & 1), ((last - 1) >> 1) & 1, ok);
+            bar_wait(bO + 8 * (last & 1), (last >> 1) & 1, ok);
+            __syncwarp();
+            tc_after();
+            const bool whole = walk.whole();
+            float *part = ws_part + (size_t)(2 * blockIdx.x + (walk.j0 == 0 ? 1 : 0)) * (MT * (D + 2));
+            if constexpr (C::COPIES == 1) {
+                const long long tk = rq.tok + tok_i;
+                const int hq = walk.h * G + g % G;
+                const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c, o);
+                    tmem_ld_wait(o);
+                    if (live && whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + tk * p.ld_out + (long long)hq * D + c);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(~0u, l[e], 1);
-            l[e] += __shfl_xor_sync(~0u, l[e], 2);
-            if (qd == 0) {
-                s_m[wn][wm * 16 + gr + 8 * e] = m[e];
-                s_l[wn][wm * 16 + gr + 8 * e] = l[e];
-            }
-        }
-        __syncthreads();
-        float *buf = reinterpret_cast<float *>(smem); // [WN][MT][D]
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = wm * 16 + gr + 8 * e;
-            float top = s_m[0][row];
+                            for (int x = 0; x < 4; ++x)
+                                b[x] = pack2<false>(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                            dst[e] = make_uint4(b[0], b[1], b[2], b[3]);
+                        }
+                    } else if (live) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(part + (size_t)row * D + c);
 #pragma unroll
-            for (int w = 1; w < C::WN; ++w)
-                top = fmaxf(top, s_m[w][row]);
-            const float f = C::WN == 1 || m[e] == -INFINITY ? 1.0f : exp2_fast(m[e] - top);
-            float *o = buf + ((size_t)wn * MT + row) * D;
-#pragma unroll
-            for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int col = C::F8 ? 16 * (d >> 1) + 4 * qd + 2 * c + (d & 1) : 8 * d + 2 * qd + c;
-                    o[col] = acc[d][2 * e + c] * f;
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
                 }
-        }
-        __syncthreads();
-        const bool whole = nt == rq.tiles;
-        float *part = ws_part + (size_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * (MT * (D + 2));
-        for (int i = tid; i < MT * (D / 4); i += kThreads) {
-            const int row = i / (D / 4), c = (i % (D / 4)) * 4;
-            const int g = rt * MT + row, ti = g / G;
-            if (ti >= rq.n)
-                continue;
-            float top = s_m[0][row];
-#pragma unroll
-            for (int w = 1; w < C::WN; ++w)
-                top = fmaxf(top, s_m[w][row]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < C::WN; ++w) {
-                const float4 x = *reinterpret_cast<const float4 *>(buf + ((size_t)w * MT + row) * D + c);
-                o.x += x.x;
-                o.y += x.y;
-                o.z += x.z;
-                o.w += x.w;
-                sum += s_m[w][row] == -INFINITY ? s_l[w][row] : s_l[w][row] * exp2_fast(s_m[w][row] - top);
-            }
-            if (whole) {
-                const float inv = sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
-                const long long t = rq.tok + ti;
-                const int hq = h * G + g % G;
-                const uint2 b = make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
-                *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + c) = b;
-                if (p.lse && c == 0)
-                    p.lse[t * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                if (live && whole && p.lse)
+                    p.lse[tk * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+                if (live && !whole) {
+                    part[MT * D + row] = m;
+                    part[MT * D + MT + row] = l;
+                }
+                tc_before();
+                soft_sync(); // s_f and the operand are free for the next segment
             } else {
-                *reinterpret_cast<float4 *>(part + (size_t)row * D + c) = o;
-                if (c == 0) {
-                    part[MT * D + row] = top;
-                    part[MT * D + MT + row] = sum;
+                // join the copies, in the operand's place (its products are done)
+                s_m[quad][row] = m;
+                s_l[quad][row] = l;
+                soft_sync();
+                float top = s_m[0][row];
+#pragma unroll
+                for (int c = 1; c < C::COPIES; ++c)
+                    top = fmaxf(top, s_m[c][row]);
+                const float f = m == -INFINITY ? 1.0f : exp2_fast(m - top); // then all zero, or NaN
+                constexpr int HALF = C::COPIES / 2;
+                float4 *buf = reinterpret_cast<float4 *>(smem) + ((quad % HALF) * MT + row) * (D / 4);
+#pragma unroll
+                for (int pass = 0; pass < 2; ++pass) {
+                    if ((quad >= HALF) == (pass == 0) && warp_live)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float4 x = make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                       __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                                float4 &b = buf[(c / 4 + e) ^ (row & 7)];
+                                if (pass)
+                                    x = make_float4(x.x + b.x, x.y + b.y, x.z + b.z, x.w + b.w);
+                                b = x;
+                            }
+                        }
+                    tc_before();
+                    soft_sync();
                 }
+                for (int k = tid; k < MT * (D / 4); k += kSoftThreads) {
+                    const int rr = k / (D / 4), c4 = k % (D / 4), gg = walk.rt * MT + rr, ti = gg / G;
+                    if (ti >= rq.n)
+                        break;
+                    const float4 *b = reinterpret_cast<const float4 *>(smem) + rr * (D / 4) + (c4 ^ (rr & 7));
+                    float4 o = b[0];
+                    if constexpr (HALF == 2) {
+                        const float4 x = b[MT * (D / 4)];
+                        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+                    }
+                    float mt = s_m[0][rr], sum = 0.0f;
+#pragma unroll
+                    for (int c = 1; c < C::COPIES; ++c)
+                        mt = fmaxf(mt, s_m[c][rr]);
+#pragma unroll
+                    for (int c = 0; c < C::COPIES; ++c)
+                        sum += s_m[c][rr] == -INFINITY ? s_l[c][rr] : s_l[c][rr] * exp2_fast(s_m[c][rr] - mt);
+                    if (whole) {
+                        const float inv = sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
+                        const long long tk = rq.tok + ti;
+                        const int hq = walk.h * G + gg % G;
+                        *reinterpret_cast<uint2 *>(p.out + tk * p.ld_out + (long long)hq * D + 4 * c4) =
+                            make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+                        if (p.lse && c4 == 0)
+                            p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (mt + log2f(sum)) * kLn2;
+                    } else {
+                        *reinterpret_cast<float4 *>(part + (size_t)rr * D + 4 * c4) = o;
+                        if (c4 == 0) {
+                            part[MT * D + rr] = mt;
+                            part[MT * D + MT + rr] = sum;
+                        }
+                    }
+                }
+                soft_sync(); // the operand's place is free for the next segment
             }
         }
-        __syncthreads();
-        u += nt;
     }
+    if (!ok)
+        set_status(p.status, SGQ_STATUS_TIMEOUT);
+    tc_before();
+    __syncthreads();
+    if (warp == kIssuer)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
 // One CTA per (token, query head): joins the parts of its row in key order.
+constexpr int kJoinThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnProblem p, int MT, int C)
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const AttnProblem p, int MT, int C)
 {
     constexpr int LPR = D / 4;              // threads per row of a part
-    constexpr int NG = kThreads / LPR;      // parts read side by side
+    constexpr int NG = kJoinThreads / LPR;      // parts read side by side
     __shared__ float4 s_o[NG][LPR];
     __shared__ float s_m[NG], s_l[NG];
     const int hq = blockIdx.x % p.Hq;
@@ -699,13 +757,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnProblem p, 
     const float *ws_part = reinterpret_cast<const float *>(static_cast<const char *>(p.workspace) + units_bytes(p.R));
     const long long U = ws_units[p.R];
     const int g = (t - q.tok) * G + hq % G, rt = g / MT, row = g % MT;
-    const long long u0 = ws_units[lo] + ((long long)h * q.row_tiles + rt) * q.tiles;
-    if (u0 + q.tiles > U)
+    const long long u0 = ws_units[lo] + ((long long)h * q.row_tiles + rt) * (q.tiles + kItemCost);
+    if (u0 + q.tiles + kItemCost > U)
         return;
     const int c0 = cta_of(U, u0, C), c1 = cta_of(U, u0 + q.tiles - 1, C);
     if (c0 == c1)
         return; // written whole
-    const int parts = U >= C ? c1 - c0 + 1 : q.tiles; // fewer units than CTAs: one each
+    const int parts = U >= C ? c1 - c0 + 1 : q.tiles; // fewer positions than CTAs: one each
     const int grp = threadIdx.x / LPR, x = threadIdx.x % LPR;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.0f;
@@ -748,25 +806,73 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnProblem p, 
         p.lse[(long long)t * p.Hq + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps, looked up once.
+EncodeTiled encoder()
+{
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<EncodeTiled>(fn);
+    }();
+    return f;
+}
+
+// (element, slot, head, page) of the cache; a box is 128 bytes of a row (64
+// where the row has no more) times `box` slots of one page and head. A
+// dimension of one entry has no stride of its own: any valid one will do.
+bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box)
+{
+    const bool f8 = c.type == SGQ_TYPE_E4M3;
+    const int es = f8 ? 1 : 2, inner = std::min(c.dim, 128 / es);
+    const cuuint64_t row = (cuuint64_t)c.dim * es;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {c.page > 1 ? (cuuint64_t)c.slot_stride * es : row,
+                                   c.heads > 1 ? (cuuint64_t)c.head_stride * es : row,
+                                   c.num_pages > 1 ? (cuuint64_t)c.page_stride * es : row};
+    const cuuint32_t boxes[4] = {(cuuint32_t)inner, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return encoder()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes,
+                     ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int KV, int MT>
 cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
 {
-    return launch_step(attn_kernel<D, KV, MT>, grid, kThreads, Cfg<D, KV, MT>::SMEM, 1, stream, p);
+    using C = Cfg<D, KV, MT>;
+    TcArgs a;
+    a.p = p;
+    a.box = 1;
+    while (a.box < 64 && p.cache.page % (2 * a.box) == 0)
+        a.box *= 2;
+    a.pitch = a.box == 1 ? 128 : D;
+    CUtensorMap kmap, vmap;
+    if (!encoder())
+        return cudaErrorNotSupported;
+    if (!encode(&kmap, p.cache, p.cache.k, a.box) || !encode(&vmap, p.cache, p.cache.v, a.box))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch_step(attn_kernel<D, KV, MT>, grid, C::THREADS, C::SMEM, 1, stream, a, kmap, vmap);
+    if (e != cudaSuccess)
+        return e;
+    return launch_step(combine_kernel<D>, (unsigned)(p.T * p.Hq), kJoinThreads, 0, 1, stream, p, MT, grid);
 }
 
 template <int D, int KV>
 cudaError_t launch_d(const AttnProblem &p, int num_sms, cudaStream_t stream)
 {
-    const int grid = std::min(2 * num_sms, kMaxGrid);
+    const int grid = std::min(num_sms, kMaxGrid);
     const int G = p.Hq / p.cache.heads;
     const long long rows = (long long)((p.T + p.R - 1) / p.R) * G;
-    const int MT = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    cudaError_t e = MT == 16   ? launch_t<D, KV, 16>(p, grid, stream)
-                    : MT == 32 ? launch_t<D, KV, 32>(p, grid, stream)
-                               : launch_t<D, KV, 64>(p, grid, stream);
-    if (e != cudaSuccess)
-        return e;
-    return launch_step(combine_kernel<D>, (unsigned)(p.T * p.Hq), kThreads, 0, 1, stream, p, MT, grid);
+    return rows <= 32   ? launch_t<D, KV, 32>(p, grid, stream)
+           : rows <= 64 ? launch_t<D, KV, 64>(p, grid, stream)
+                        : launch_t<D, KV, 128>(p, grid, stream);
 }
 
 } // namespace
