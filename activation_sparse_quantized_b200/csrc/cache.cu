@@ -357,7 +357,7 @@ cudaError_t launch_plan(const PlanProblem &p, int num_sms, cudaStream_t stream)
     int ctas = 1;
     while (ctas < 8 && ctas * kPlanThreads < p.max_tokens)
         ctas *= 2;
-    return launch_step(plan_kernel, ctas, kPlanThreads, (size_t)(4 * p.R + 1) * 4, ctas, stream, p);
+    return launch_step(plan_kernel, dim3(ctas), kPlanThreads, (size_t)(4 * p.R + 1) * 4, ctas, stream, p);
 }
 
 cudaError_t launch_write(const WriteProblem &p, int num_sms, cudaStream_t stream)
@@ -366,7 +366,7 @@ cudaError_t launch_write(const WriteProblem &p, int num_sms, cudaStream_t stream
     const long long per =
         (long long)((p.q ? p.Hq : 0) + 2 * p.cache.heads) * (p.cache.dim / 16);
     const long long grid = (p.T * per + kWriteThreads - 1) / kWriteThreads;
-    return launch_step(write_kernel, (unsigned)grid, kWriteThreads, 0, 1, stream, p);
+    return launch_step(write_kernel, dim3((unsigned)grid), kWriteThreads, 0, 1, stream, p);
 }
 
 } // namespace sgq

@@ -179,9 +179,9 @@ cudaError_t launch_t(const NormProblem &p, cudaStream_t stream)
     const int k = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
     const int block = ((chunks + k - 1) / k + 31) / 32 * 32;
     switch (k) {
-    case 1: return launch_step(norm_kernel<AT, RT, WT, 1>, p.B, block, 0, 1, stream, p);
-    case 2: return launch_step(norm_kernel<AT, RT, WT, 2>, p.B, block, 0, 1, stream, p);
-    default: return launch_step(norm_kernel<AT, RT, WT, 4>, p.B, block, 0, 1, stream, p);
+    case 1: return launch_step(norm_kernel<AT, RT, WT, 1>, dim3(p.B), block, 0, 1, stream, p);
+    case 2: return launch_step(norm_kernel<AT, RT, WT, 2>, dim3(p.B), block, 0, 1, stream, p);
+    default: return launch_step(norm_kernel<AT, RT, WT, 4>, dim3(p.B), block, 0, 1, stream, p);
     }
 }
 

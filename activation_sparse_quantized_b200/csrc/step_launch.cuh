@@ -10,7 +10,7 @@ namespace sgq {
 namespace {
 
 template <typename Kern, typename... Args>
-cudaError_t launch_step(Kern kern, unsigned grid, int block, size_t smem, int cluster,
+cudaError_t launch_step(Kern kern, dim3 grid, int block, size_t smem, int cluster,
                         cudaStream_t stream, const Args &...args)
 {
     if (smem > 48 * 1024) {
@@ -20,7 +20,7 @@ cudaError_t launch_step(Kern kern, unsigned grid, int block, size_t smem, int cl
             return err;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

@@ -48,14 +48,27 @@ __device__ __forceinline__ long long cost_of(const Request &q, int Hkv)
     return q.tiles ? (long long)Hkv * q.row_tiles * (q.tiles + kItemCost) : 0;
 }
 
-// Start of CTA c's run of C equal ones, and the CTA whose run holds position u.
+// Start of CTA c's run of C equal ones (1 <= C <= U), and the CTA whose run
+// holds position u.
 __device__ __forceinline__ long long run_start(long long U, int c, int C) { return U * c / C; }
 __device__ __forceinline__ int cta_of(long long U, long long u, int C)
 {
     return (int)(((u + 1) * C - 1) / U);
 }
 
-__host__ __device__ inline size_t units_bytes(int R) { return ((size_t)(R + 1) * 8 + 255) / 256 * 256; }
+// An item that CTA c starts and others go on with, for the kernel that joins
+// its parts: those of CTAs c, c + 1, ..., c + parts - 1 (parts = 0: none).
+struct __align__(32) Split {
+    int parts, tok, n, h, rt;
+};
+
+// The part that CTA c leaves of the item it starts (which = 1) or goes on with
+// (which = 0): MT rows of D sums, then the rows' references, then their sums.
+__device__ __forceinline__ float *part_of(const AttnProblem &p, int c, int which, int MT, int D)
+{
+    return reinterpret_cast<float *>(static_cast<char *>(p.workspace) + kMaxGrid * sizeof(Split)) +
+           (size_t)(2 * c + which) * (MT * (D + 2));
+}
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -84,15 +97,30 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
+// The first 64 bits of token i's tree words.
+__device__ __forceinline__ uint64_t tree_bits(const AttnProblem &p, const Request &q, int i)
+{
+    if (!p.tree)
+        return 0;
+    const uint32_t *w = p.tree + (long long)(q.tok + i) * p.tree_words;
+    return w[0] | (p.tree_words > 1 ? (uint64_t)w[1] << 32 : 0);
+}
+
 // The 64 keys from kb0 on, and before `end`, that token i sees, bit by key: all
-// of the context, and of the drafted tokens those its tree words name (no
-// tree: itself and the ones before it).
-__device__ __forceinline__ uint64_t visible(const AttnProblem &p, const Request &q, int i, int kb0, int end)
+// of the context, and of the drafted tokens those its tree words name (`first`:
+// tree_bits; no tree: itself and the ones before it).
+__device__ __forceinline__ uint64_t visible(const AttnProblem &p, const Request &q, int i,
+                                            uint64_t first, int kb0, int end)
 {
     const int start = kb0 - q.len;
     const int s = max(start, 0);
     uint64_t d = 0;
-    if (p.tree) {
+    if (!p.tree) {
+        const int ones = i + 1 - s;
+        d = ones >= 64 ? ~0ull : ones > 0 ? (1ull << ones) - 1 : 0ull;
+    } else if (s == 0 || p.tree_words <= 2) {
+        d = s < 64 ? first >> s : 0ull;
+    } else {
         const uint32_t *w = p.tree + (long long)(q.tok + i) * p.tree_words;
         const int k = s >> 5, sh = s & 31;
         const uint64_t w0 = k < p.tree_words ? w[k] : 0u;
@@ -101,9 +129,6 @@ __device__ __forceinline__ uint64_t visible(const AttnProblem &p, const Request 
         d = (w0 | (w1 << 32)) >> sh;
         if (sh)
             d |= w2 << (64 - sh);
-    } else {
-        const int ones = i + 1 - s;
-        d = ones >= 64 ? ~0ull : ones > 0 ? (1ull << ones) - 1 : 0ull;
     }
     if (start < 0) {
         const int sh = -start;
@@ -120,6 +145,7 @@ struct Walk {
     int j0 = 0, nu = 0;
     Request rq{};
     long long base = 0, u = 0, u_end = 0; // cost before request r, the run
+    long long item0 = 0;                  // cost before the item
 
     __device__ __forceinline__ int key_end() const { return min(rq.keys, (j0 + nu) * kBN); }
     __device__ __forceinline__ bool whole() const { return nu == rq.tiles; }
@@ -132,15 +158,19 @@ struct Walk {
                 base += cost_of(rq, p.cache.heads);
                 rq = request_of(p, ++r, G, MT, bits);
             }
-            const long long in_r = u - base, item = in_r / (rq.tiles + kItemCost);
-            const int p0 = (int)(in_r - item * (rq.tiles + kItemCost));
+            const long long in_r = u - base;
+            const int cost = rq.tiles + kItemCost;
+            // (a 32-bit division where it will do: 64-bit ones take a call)
+            const long long item = in_r >> 31 ? in_r / cost : (long long)((uint32_t)in_r / (uint32_t)cost);
+            const int p0 = (int)(in_r - item * cost);
             const int p1 = (int)min((long long)(rq.tiles + kItemCost), p0 + (u_end - u));
             u += p1 - p0;
             if (p0 >= rq.tiles)
                 continue;
+            item0 = base + item * cost;
             j0 = p0;
             nu = min(p1, rq.tiles) - p0;
-            h = (int)(item / rq.row_tiles);
+            h = item >> 31 ? (int)(item / rq.row_tiles) : (int)((uint32_t)item / (uint32_t)rq.row_tiles);
             rt = (int)(item - (long long)h * rq.row_tiles);
             return true;
         }
