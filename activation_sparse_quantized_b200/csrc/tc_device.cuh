@@ -30,10 +30,11 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
-// Waits for the phase of the given parity to complete, for at most kBarWaitNs
-// of wall time. A thread whose wait gave up has ok = false and waits no more,
-// so that a broken hand-off ends the kernel within a fraction of a second.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, bool &ok)
+// Waits for the phase of the given parity to complete, for at most `limit` of
+// wall time. A thread whose wait gave up has ok = false and waits no more, so
+// that a broken hand-off ends the kernel within a fraction of a second.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, bool &ok,
+                                         unsigned long long limit = kBarWaitNs)
 {
     unsigned long long t0 = 0;
     while (ok) {
@@ -50,7 +51,7 @@ __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, bool &ok
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
         if (t0 == 0)
             t0 = t;
-        else if (t - t0 > kBarWaitNs)
+        else if (t - t0 > limit)
             ok = false;
     }
 }
@@ -74,16 +75,17 @@ __device__ __forceinline__ void fence_async_smem()
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Descriptor of a 128-byte-swizzled operand in shared memory (sm_100 form).
-// K-major: sbo = stride of 8-row groups. MN-major: lbo = stride of 64-element
-// blocks along M or N, sbo = stride of 8-row groups along K.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// Descriptor of a swizzled operand in shared memory (sm_100 form); layout 2:
+// 128-byte swizzle, 4: 64-byte. K-major: sbo = stride of 8-row groups. MN-major:
+// lbo = stride of swizzle-wide blocks along M or N, sbo = of 8-row groups along K.
+__device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout = 2)
 {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)layout << 61);
 }
 
-// Instruction descriptor of tcgen05.mma kind::f16 with fp32 sums, M = 128.
+// Instruction descriptor of tcgen05.mma kind::f16 with fp32 sums, M = 128
+// (fp16 operands' code is also kind::f8f6f4's for e4m3).
 __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, bool b_mn_major, int n)
 {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |
@@ -94,6 +96,15 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+// The same on 8-bit operands (32 along K).
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
@@ -139,6 +150,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
                  "%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
                  SGQ_I8(r, 0), SGQ_I8(r, 8), SGQ_I8(r, 16), SGQ_I8(r, 24)
                  : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
+                 "%12,%13,%14,%15}, [%16];"
+                 : SGQ_R8(r, 0), SGQ_R8(r, 8)
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : SGQ_RW8(r, 0), SGQ_RW8(r, 8)::"memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)

@@ -18,60 +18,72 @@
 // workspace, and join_kernel joins them in order; a whole item is written out
 // directly.
 //
-// Both products are tcgen05.mma of 128 rows and 128 keys. Eight warps:
-//  * one looks up the pages and copies keys and values by the box
-//    (cp.async.bulk.tensor, 128-byte swizzle), two ring slots per 128 keys;
-//    what lies behind a segment's keys, and bad pages, is filled with zeros by
-//    a box outside the map;
-//  * one thread of another issues S = Q K^T (both from shared memory) into one
-//    of two accumulators, one tile ahead and across segments, and O += P V
-//    with P read from tensor memory, where it takes S's place;
-//  * four, one accumulator row per thread, turn S into P. Their reference for
-//    the exponent moves only when a row's maximum outgrows it by 2^8, so O is
-//    rescaled rarely;
-//  * two fetch the next segment's Q, look through the values next to the end,
-//    and make 8-bit keys and values fp16 (exact) on their way to the slots the
-//    products read.
+// Both products are tcgen05.mma of 128 rows and 128 keys. The warps:
+//  * one walks the run, looks up the pages and copies keys and values by the
+//    box (cp.async.bulk.tensor, swizzled), two ring slots per 128 keys; what
+//    lies behind a segment's keys, and bad pages, is filled with zeros by a
+//    box outside the map;
+//  * one thread issues S = Q K^T (both from shared memory) into one of two
+//    accumulators, one tile ahead and across segments, and O += P V with P
+//    read from tensor memory, where it takes S's place;
+//  * two groups of four take the tiles in turn, one accumulator row per
+//    thread, turn S into P and have an O of their own, so that one group's
+//    exponentials overlap the other's. The reference for the exponent moves
+//    only when a row's maximum outgrows it by 2^8, so O is rescaled rarely. A
+//    segment of one tile is one group's alone;
+//  * the rest fetch the next segment's Q and look through the values next to
+//    the end. With 8-bit keys and values q is split into two 8-bit parts, so
+//    that S is a product of 8-bit operands as they lie, and these warps make
+//    the values fp16 (exact): weights of 8 bits would lose a long row's tail.
 // A tile of 32 or 64 rows (MT) is laid into the 128 several times, and copy c
 // takes part c of the keys, its P zero elsewhere: the copies' O are partial
-// sums over the keys, joined at the segment's end. All four softmax warps then
-// share the exponentials of a few rows.
+// sums over the keys, joined at the segment's end with the other group's. All
+// the softmax warps then share the exponentials of a few rows.
 //
 // Every wait on a barrier is bounded by 0.2 s; one that runs out sets
-// SGQ_STATUS_TIMEOUT, the thread waits on nothing more and the kernel runs to
-// its end.
+// SGQ_STATUS_TIMEOUT, the thread waits for no data any more and the kernel runs
+// to its end. The segments are passed on all the same (those waits, bounded by
+// 2 s, outlast the others), so the warps of a group still meet at their
+// barriers.
 #include "step_launch.cuh"
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
 
 #include <algorithm>
+#include <cuda_fp8.h>
 
 namespace sgq {
 
 namespace {
 
 constexpr int kTile = 128; // keys per product
-constexpr int kSoftThreads = 128, kAuxThreads = 64, kThreads = 256;
-constexpr int kSoftWarps = 4, kProducer = 4, kIssuer = 5, kAux = 6; // warps
-constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, O
+constexpr int kGroup = 128; // threads of a softmax group
+constexpr int kSoftWarps = 8, kProducer = 8, kIssuer = 9, kAux = 10; // warps
+constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
+constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
+constexpr int kTiles = 16;      // tiles that are
+constexpr unsigned long long kSegWaitNs = 2000000000ull;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_;
     static constexpr bool F8 = KV == SGQ_TYPE_E4M3;
-    static constexpr int COPIES = 128 / MT, KW = kTile / COPIES; // copies of the rows, keys of each
-    static constexpr int SUB = kTile * 128;                      // 128 rows x 64 elements, swizzled
+    static constexpr int AUX = F8 ? 4 : 2, THREADS = 32 * (kAux + AUX);
+    static constexpr int COPIES = 128 / MT, NCH = 4 / COPIES; // copies of the rows, 32-key chunks of each
+    static constexpr int SUB = kTile * 128;                   // 128 rows x 128 bytes, swizzled
     static constexpr int NSUB = D / 64;
-    static constexpr int SLOT = NSUB * SUB;                      // 128 keys (or values), 16 bits
-    static constexpr int RAW = kTile * 128;                      // the same, 8 bits (see TcArgs::pitch)
-    static constexpr int NS = F8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int RS = F8 ? 4 : 0;
-    static constexpr int Q = SLOT, JOIN = MT == 128 ? 0 : 128 * 32 * 4;
-    static constexpr int BARS = 2 * NS + 2 * RS + 12;
-    static constexpr int SMEM = 1024 + Q + JOIN + NS * SLOT + RS * RAW + BARS * 8;
-    static constexpr int LOADS = F8 ? RS : NS; // slots the copies go to
-    static_assert(SMEM <= 227 * 1024 - 4096, "room for the static arrays");
+    static constexpr int SLOT = NSUB * SUB;                   // 128 keys (or values), 16 bits
+    static constexpr int KV_BYTES = F8 ? 96 * 1024 : D == 128 ? 5 * SLOT : 10 * SLOT; // the ring of copies
+    static constexpr int MAX_SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
+    static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
+    static constexpr int Q = F8 ? 2 * SUB : SLOT, JOIN = 2 * kGroup * 64;
+    static constexpr int BARS = 2 * MAX_SLOTS + 2 * NV + 6 + 3 * kRing + 2;
+    static constexpr int SMEM = 1024 + Q + KV_BYTES + NV * SLOT + JOIN + BARS * 8;
+    static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
+    // copies run ahead of the softmax by the ring's tiles, 8-bit ones by NV more and the
+    // one in between: its entries live that long, those of tail tiles without the ring
+    static_assert(MAX_SLOTS / 2 + NV + 2 <= kTiles && (F8 ? NV + 1 : MAX_SLOTS / 2 + 1) <= kRing, "ring entries");
 };
 
 struct TcArgs {
@@ -81,16 +93,55 @@ struct TcArgs {
                // of one 64-byte row leaves the other 64 empty
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+// What a CTA's warps need of a segment (nt = 0: the run has ended).
+struct Seg {
+    int nt;                     // tiles
+    int tok, n, len;            // the request's first row, new tokens, cached ones
+    int key0, end;              // its keys
+    int h, rt;                  // key head, row tile
+    int first_tail, tail_index; // tiles from here on reach the drafted tokens or the end; the
+                                // first one's number among the run's
+    int whole, which;           // the whole item; else which part it is
+};
 
-// Byte offset of 16-byte chunk c (8 elements) of row r of an operand.
+// A place in a ring of n slots that every warp walks in steps of one or two.
+struct Ring {
+    int s;
+    uint32_t ph;
+    __device__ __forceinline__ void step(int by, int n)
+    {
+        s += by;
+        if (s >= n) {
+            s -= n;
+            ph ^= 1;
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void named_sync(int bar)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Byte offset of 16-byte chunk c of row r of an operand of 16-bit elements.
 __device__ __forceinline__ uint32_t op_off(int r, int c)
 {
     return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 template <int D, int KV, int MT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     attn_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap)
 {
@@ -101,17 +152,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ long long s_scan[4], s_first;
     __shared__ int s_r;
     __shared__ Request s_rq;
-    __shared__ float s_m[C::COPIES][MT], s_l[C::COPIES][MT];
+    __shared__ Seg s_seg[kRing];
+    __shared__ float s_m[2 * C::COPIES][MT], s_l[2 * C::COPIES][MT];
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
-    __shared__ uint32_t s_bad[8][4];                     // keys without a page of the last tiles, bit by key
-    __shared__ uint32_t s_odd[4][4];                     // values that are not finite of the last tail tiles
-    __shared__ int s_acc[2];                             // the first product of a segment adds to O
+    __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
+    __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
+    __shared__ int s_acc[2];                             // a group's first product of a segment adds to O
     uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    const uint32_t sQ = smem_u32(smem), sKV = sQ + C::Q, sRaw = sKV + C::NS * C::SLOT;
-    const uint32_t sJoin = sRaw + C::RS * C::RAW, bars = sJoin + C::JOIN;
-    const uint32_t bFull = bars, bEmpty = bFull + 8 * C::NS, bRFull = bEmpty + 8 * C::NS, bREmpty = bRFull + 8 * C::RS;
-    const uint32_t bS = bREmpty + 8 * C::RS, bP = bS + 16, bO = bP + 16, bTail = bO + 16;
-    const uint32_t bQ = bTail + 32, bQFree = bQ + 8;
+    const uint32_t sQ = smem_u32(smem), sKV = sQ + C::Q, sV = sKV + C::KV_BYTES, sJoin = sV + C::NV * C::SLOT;
+    const uint32_t bFull = sJoin + C::JOIN, bEmpty = bFull + 8 * C::MAX_SLOTS;
+    const uint32_t bVFull = bEmpty + 8 * C::MAX_SLOTS, bVEmpty = bVFull + 8 * C::NV;
+    const uint32_t bS = bVEmpty + 8 * C::NV, bP = bS + 16, bO = bP + 16;
+    const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8;
+    // the ring of copies: keys in one slot, values in the next
+    const uint32_t slot_bytes = C::F8 ? kTile * a.pitch : C::SLOT;
+    const int slots = C::F8 ? (a.pitch == D ? C::MAX_SLOTS : C::KV_BYTES / (kTile * 128)) : C::MAX_SLOTS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.cache.heads, G = p.Hq / Hkv;
 
@@ -119,40 +174,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else if (warp == kProducer && lane == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-            bar_init(bFull + 8 * s, C::F8 ? 2 : 1);
-            bar_init(bEmpty + 8 * s, 1);
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+        for (int s = 0; s < C::MAX_SLOTS; ++s) {
+            bar_init(bFull + 8 * s, 1);
+            // read by the products and followed by the aux warps; 8-bit keys by the
+            // products alone, 8-bit values by the aux warps alone
+            bar_init(bEmpty + 8 * s, !C::F8 ? 1 + C::AUX : s & 1 ? C::AUX : 1);
         }
-        for (int s = 0; s < C::RS; ++s) {
-            bar_init(bRFull + 8 * s, 1);
-            bar_init(bREmpty + 8 * s, 2);
+        for (int s = 0; s < C::NV; ++s) {
+            bar_init(bVFull + 8 * s, C::AUX);
+            bar_init(bVEmpty + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(bS + 8 * b, 1);
-            bar_init(bP + 8 * b, kSoftWarps);
+            bar_init(bP + 8 * b, 4);
             bar_init(bO + 8 * b, 1);
             s_acc[b] = 0;
         }
-        for (int b = 0; b < 4; ++b)
-            bar_init(bTail + 8 * b, 2);
-        bar_init(bQ, 2);
+        for (int b = 0; b < kRing; ++b) {
+            bar_init(bTail + 8 * b, C::AUX);
+            bar_init(bSeg + 8 * b, 1);
+            bar_init(bSegFree + 8 * b, kSoftWarps);
+        }
+        bar_init(bQ, C::AUX);
         bar_init(bQFree, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_r = p.R;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     }
     grid_launch_dependents();
     grid_dependency_wait();
 
     // The requests' costs, their sum U, and this CTA's run of [0, U).
     int bits = 0;
-    bool ok = true;
-    const int per = (p.R + kSoftThreads - 1) / kSoftThreads;
+    bool ok = true, led = true; // no wait for data, for a segment ran out
+    const int per = (p.R + kGroup - 1) / kGroup;
     const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
     long long mine = 0, at = 0;
     Request rq0{};
-    if (warp < kSoftWarps) {
+    if (warp < 4) {
         for (int r = r0; r < r1; ++r) {
             rq0 = request_of(p, r, G, MT, bits);
             mine += cost_of(rq0, Hkv);
@@ -176,21 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     const long long U = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
     const int ctas = (int)min((long long)gridDim.x, U); // those with work
-    Walk walk;
+    long long u = 0, u_end = 0;
     if ((int)blockIdx.x < ctas) {
-        walk.u = run_start(U, blockIdx.x, ctas);
-        walk.u_end = run_start(U, blockIdx.x + 1, ctas);
+        u = run_start(U, blockIdx.x, ctas);
+        u_end = run_start(U, blockIdx.x + 1, ctas);
     }
-    if (warp < kSoftWarps && walk.u < walk.u_end) {
+    if (warp < 4 && u < u_end) {
         for (int w = 0; w < warp; ++w)
             at += s_scan[w];
-        if (walk.u >= at && walk.u < at + mine) {
+        if (u >= at && u < at + mine) {
             int r = r0, none = 0;
             if (per > 1)
                 for (; r < r1; ++r) {
                     rq0 = request_of(p, r, G, MT, none);
                     const long long n = cost_of(rq0, Hkv);
-                    if (walk.u < at + n)
+                    if (u < at + n)
                         break;
                     at += n;
                 }
@@ -200,73 +259,110 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    walk.r = s_r;
-    walk.base = s_first;
-    walk.rq = s_rq;
 
     if (warp == kProducer) {
-        // ---- pages -> slots ----------------------------------------------
+        // ---- the run's segments; pages -> slots ------------------------------
         // Lane x of round j copies piece x + 32 j of a slot: a box of `box` rows
         // and 128 bytes (one round for pages of at least 8 slots). The pages of
         // the next two tiles are looked up ahead.
-        const uint32_t full = C::F8 ? bRFull : bFull, empty = C::F8 ? bREmpty : bEmpty;
-        const uint32_t dst0 = C::F8 ? sRaw : sKV;
+        Walk walk;
+        walk.u = u;
+        walk.u_end = u_end;
+        if (u < u_end) {
+            walk.r = s_r;
+            walk.base = s_first;
+            walk.rq = s_rq;
+        }
         const uint32_t bytes = C::F8 ? kTile * D : C::SLOT; // of one slot's boxes
-        constexpr uint32_t STEP = C::F8 ? C::RAW : C::SLOT;
-        constexpr int PARTS = C::F8 ? 1 : C::NSUB; // boxes side by side in a row
+        constexpr int PARTS = C::F8 ? 1 : C::NSUB;          // boxes side by side in a row
         const int row_bytes = C::F8 ? a.pitch : 128;
         const int pieces = kTile / a.box * PARTS, rounds = (pieces + 31) / 32;
         const int page = p.cache.page, page_up = kTile / page, slot_up = kTile % page;
-        int i = 0, issued = 0; // tiles, slots so far
-        while (walk.next(p, G, MT)) {
-            const int32_t *table = p.table + (long long)walk.r * p.table_ld;
+        auto step = [&](int &g, int &s) { // one tile on
+            g += page_up;
+            s += slot_up;
+            if (s >= page) {
+                s -= page;
+                ++g;
+            }
+        };
+        Ring ring{0, 0}, seg{0, 0};
+        Split split[2] = {};
+        int i = 0, tails = 0, issued = 0; // tiles, tail tiles, slots so far
+        for (;;) {
+            const bool more = __all_sync(~0u, ok) && walk.next(p, G, MT);
+            const int nt = more ? (walk.nu + 1) / 2 : 0;
             const int key0 = walk.j0 * kBN, end = walk.key_end();
-            const int nt = (walk.nu + 1) / 2;
+            const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
+            bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSegWaitNs);
+            __syncwarp();
+            if (lane == 0) {
+                Seg &sg = s_seg[seg.s];
+                sg.nt = nt;
+                sg.tok = walk.rq.tok;
+                sg.n = walk.rq.n;
+                sg.len = walk.rq.len;
+                sg.key0 = key0;
+                sg.end = end;
+                sg.h = walk.h;
+                sg.rt = walk.rt;
+                sg.first_tail = first_tail;
+                sg.tail_index = tails;
+                sg.whole = walk.whole();
+                sg.which = walk.j0 == 0;
+                bar_arrive(bSeg + 8 * seg.s);
+            }
+            seg.step(1, kRing);
+            if (!more)
+                break;
+            tails += max(0, nt - first_tail);
+            const int32_t *table = p.table + (long long)walk.r * p.table_ld;
             // this lane's box of round 0: page index, slot in it, ids of the next tiles
             const int first = key0 + lane / PARTS * a.box;
             int pg = first / page, sl = first - pg * page;
             auto look = [&](int t, int at_page) {
                 return lane < pieces && t < nt && first + t * kTile < end ? table[at_page] : -1;
             };
-            int pg_next = pg, sl_next = sl; // one tile on
-            auto step = [&](int &g, int &s) {
-                g += page_up;
-                s += slot_up;
-                if (s >= page) {
-                    s -= page;
-                    ++g;
-                }
-            };
+            int pg_next = pg, sl_next = sl;
             int id0 = look(0, pg);
             step(pg_next, sl_next);
             int id1 = look(1, pg_next);
+            if (!walk.whole()) { // a part for join_kernel
+                Split &sp = split[walk.j0 == 0];
+                sp.c0 = cta_of(U, walk.item0, ctas);
+                sp.parts = cta_of(U, walk.item0 + walk.rq.tiles - 1, ctas) - sp.c0 + 1;
+                sp.tok = walk.rq.tok;
+                sp.n = walk.rq.n;
+                sp.h = walk.h;
+                sp.rt = walk.rt;
+            }
             for (int t = 0; t < nt; ++t, ++i) {
                 int pg2 = pg_next, sl2 = sl_next;
                 step(pg2, sl2);
                 const int id2 = look(t + 2, pg2);
+                uint32_t *bad = s_bad[i % kTiles];
                 if (lane < 4)
-                    s_bad[i & 7][lane] = 0;
+                    bad[lane] = 0;
                 // round 0's box; its page is waited for here
-                const int key = first + t * kTile;
-                const bool want = lane < pieces && key < end;
+                const bool want = lane < pieces && first + t * kTile < end;
                 const bool good = want && id0 >= 0 && id0 < p.cache.num_pages;
                 const int pid = good ? id0 : p.cache.num_pages; // outside the map: zeros
                 const int slot = good ? sl : 0;
                 bool any = __any_sync(~0u, want && !good);
                 __syncwarp();
-                if (any && want && !good && lane % PARTS == 0)
+                if (want && !good && lane % PARTS == 0)
                     for (int k = 0; k < a.box; ++k) {
                         const int b = lane / PARTS * a.box + k;
-                        atomicOr(&s_bad[i & 7][b >> 5], 1u << (b & 31));
+                        atomicOr(&bad[b >> 5], 1u << (b & 31));
                     }
-                for (int j = 1; j < rounds; ++j) { // boxes of fewer than 8 rows: their keys without a page
+                for (int j = 1; j < rounds; ++j) { // boxes of fewer than 8 rows
                     const int b = (lane + 32 * j) / PARTS, kb = key0 + t * kTile + b * a.box;
                     if (kb < end) {
                         const int id = table[kb / page];
                         if (id < 0 || id >= p.cache.num_pages) {
                             any = true;
                             for (int k = 0; k < a.box; ++k)
-                                atomicOr(&s_bad[i & 7][(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
+                                atomicOr(&bad[(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
                         }
                     }
                 }
@@ -275,32 +371,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int n = 2 * i + kv, s = n % C::LOADS;
-                    if (n >= C::LOADS)
-                        bar_wait(empty + 8 * s, (n / C::LOADS - 1) & 1, ok);
+                    bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
                     if (!__all_sync(~0u, ok)) {
                         ok = false;
                         break;
                     }
-                    issued = n + 1;
+                    ++issued;
+                    const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
                     if (lane == 0)
-                        bar_expect(full + 8 * s, bytes);
+                        bar_expect(full, bytes);
                     __syncwarp();
                     const CUtensorMap *map = kv ? &vmap : &kmap;
-                    const uint32_t dst = dst0 + s * STEP;
                     if (lane < pieces)
                         tma_load_4d(dst + (lane % PARTS) * C::SUB + lane / PARTS * a.box * row_bytes, map, lane % PARTS * 64, slot,
-                                    walk.h, pid, full + 8 * s);
+                                    walk.h, pid, full);
                     for (int j = 1; j < rounds; ++j) {
                         const int x = lane + 32 * j, b = x / PARTS, kb = key0 + t * kTile + b * a.box;
                         int id = kb < end ? table[kb / page] : -1;
                         if (id < 0 || id >= p.cache.num_pages)
                             id = p.cache.num_pages;
                         tma_load_4d(dst + (x % PARTS) * C::SUB + b * a.box * row_bytes, map, x % PARTS * 64, kb % page, walk.h, id,
-                                    full + 8 * s);
+                                    full);
                     }
+                    ring.step(1, slots);
                 }
-                pg = pg_next;
                 sl = sl_next;
                 pg_next = pg2;
                 sl_next = sl2;
@@ -308,59 +402,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 id1 = id2;
             }
         }
+        if (lane < 2)
+            static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split[1] : split[0];
         // every copy has landed before the CTA ends, whatever went wrong
         bool landed = true;
-        for (int n = max(0, issued - C::LOADS); n < issued; ++n)
-            bar_wait(full + 8 * (n % C::LOADS), (n / C::LOADS) & 1, landed);
+        for (int n = max(0, issued - slots); n < issued; ++n)
+            bar_wait(bFull + 8 * (n % slots), (n / slots) & 1, landed);
         ok = ok && landed;
     } else if (warp == kIssuer) {
         // ---- the products ------------------------------------------------
         if (lane == 0) {
             constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
-            const uint64_t dq = desc_sw128(sQ, 16, 1024);
-            int seg = 0, left = 0, i = 0; // segments begun, their tiles without scores, tiles
+            Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
+            uint32_t q_ph = 0;
+            int left = 0, nt = 0; // tiles of the segment without scores, all of them
             // The scores of tile n, the next one; false when there is none.
             auto scores = [&](int n) -> bool {
                 if (left == 0) {
-                    if (!walk.next(p, G, MT))
+                    bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+                    left = led ? *(volatile int *)&s_seg[seg.s].nt : 0;
+                    if (left == 0)
                         return false;
-                    left = (walk.nu + 1) / 2;
-                    bar_wait(bQ, seg & 1, ok);
-                    ++seg;
+                    nt = left;
+                    seg.step(1, kRing);
+                    bar_wait(bQ, q_ph, ok);
+                    q_ph ^= 1;
                 }
                 --left;
-                const int s = 2 * n % C::NS;
-                bar_wait(bFull + 8 * s, (2 * n / C::NS) & 1, ok);
+                bar_wait(bFull + 8 * kr.s, kr.ph, ok);
                 tc_after();
-                const uint64_t dk = desc_sw128(sKV + s * C::SLOT, 16, 1024);
+                const uint32_t d = tmem + (n & 1) * kTile, ka = sKV + kr.s * slot_bytes;
+                if constexpr (C::F8) {
+                    // q's two parts one after the other
+                    const uint64_t dq = op_desc(sQ, 16, 1024);
+                    const uint64_t dk = op_desc(ka, 16, 8 * a.pitch, a.pitch == 128 ? 2 : 4);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t step = (uint64_t)(((k >> 2) * C::SUB + (k & 3) * 32) >> 4);
-                    mma_ss(tmem + (n & 1) * kTile, dq + step, dk + step, idS, k > 0);
+                    for (int k = 0; k < D / 32; ++k) {
+                        mma_ss_f8(d, dq + 2 * k, dk + 2 * k, idS, k > 0);
+                        mma_ss_f8(d, dq + (C::SUB >> 4) + 2 * k, dk + 2 * k, idS, 1);
+                    }
+                } else {
+                    const uint64_t dq = op_desc(sQ, 16, 1024), dk = op_desc(ka, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t st = (uint64_t)(((k >> 2) * C::SUB + (k & 3) * 32) >> 4);
+                        mma_ss(d, dq + st, dk + st, idS, k > 0);
+                    }
                 }
-                tc_commit(bEmpty + 8 * s);
+                tc_commit(bEmpty + 8 * kr.s);
                 tc_commit(bS + 8 * (n & 1));
                 if (left == 0)
                     tc_commit(bQFree);
+                kr.step(2, slots);
                 return true;
             };
-            bool first = true, more = scores(0);
+            int i = 0, t = 0, nt_i = 0; // tile, its number in its segment, that one's tiles
+            bool more = scores(0);
+            nt_i = nt;
             while (more) {
-                const bool last = left == 0; // of its segment
                 more = scores(i + 1);
-                const int n = 2 * i + 1, s = n % C::NS;
-                bar_wait(bFull + 8 * s, (n / C::NS) & 1, ok);
+                const uint32_t vfull = C::F8 ? bVFull + 8 * (i & 1) : bFull + 8 * vr.s;
+                bar_wait(vfull, C::F8 ? (i >> 1) & 1 : vr.ph, ok);
                 bar_wait(bP + 8 * (i & 1), (i >> 1) & 1, ok);
                 tc_after();
-                const uint32_t add = !first || *(volatile int *)&s_acc[i & 1];
-                const uint64_t dv = desc_sw128(sKV + s * C::SLOT, C::SUB, 1024);
+                const uint32_t add = t >= 2 || *(volatile int *)&s_acc[i & 1];
+                const uint32_t va = C::F8 ? sV + (i & 1) * C::SLOT : sKV + vr.s * slot_bytes;
+                const uint64_t dv = op_desc(va, C::SUB, 1024);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + kColO, tmem + (i & 1) * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
-                tc_commit(bEmpty + 8 * s);
+                    mma_ts(tmem + kColO + (i & 1) * 128, tmem + (i & 1) * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
+                tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s);
                 tc_commit(bO + 8 * (i & 1));
-                first = last;
+                vr.step(2, slots);
                 ++i;
+                if (++t == nt_i) {
+                    t = 0;
+                    nt_i = nt;
+                }
             }
             // every product is complete before the tensor memory is freed
             bool done = true;
@@ -372,222 +490,268 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kAux) {
-        // ---- Q, the values next to the end, 8-bit slots -> fp16 slots --------
+        // ---- Q, the values next to the end, 8-bit values -> fp16 ---------------
+        constexpr int AT = 32 * C::AUX;
         const int ct = tid - 32 * kAux;
-        int i = 0, seg = 0, tail = 0;
-        while (walk.next(p, G, MT)) {
-            const Request &rq = walk.rq;
-            // Q, once per copy of the rows. With 8-bit keys q becomes fp16, each
-            // row by the power of two that brings its largest value into
-            // [2^7, 2^8): exact for values down to 2^-21 of that, below it off
-            // by at most 2^-33 of it. A negative scale's sign goes to q, so that
-            // the largest score is the largest exponent.
-            constexpr int CH = D / 8, N = 8;
+        Ring seg{0, 0}, vr{C::F8 ? 1 : 0, 0};
+        uint32_t free_ph = 1; // the operand is free at first
+        int i = 0, segs = 0;
+        for (;;) {
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            __syncwarp();
+            const Seg sg = s_seg[seg.s];
+            if (!led || sg.nt == 0)
+                break;
+            seg.step(1, kRing);
+            // Q, once per copy of the rows. With 8-bit keys each row is scaled by
+            // the power of two that brings its largest value into [2^7, 2^8) and
+            // split in two 8-bit parts, 4 bits each of its 8: exact for values
+            // down to 2^-2, below it off by at most 2^-10, i.e. 2^-17 of the
+            // largest. A negative scale's sign goes to q, so that the largest
+            // score is the largest exponent.
+            constexpr int CH = D / 8, ALL = MT * CH / AT, N = ALL < 8 ? ALL : 8;
             const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
-            bool waited = false;
 #pragma unroll 1
-            for (int k0 = 0; k0 < MT * CH / kAuxThreads; k0 += N) {
+            for (int k0 = 0; k0 < ALL; k0 += N) {
                 uint4 v[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * kAuxThreads, g = walk.rt * MT + idx / CH, ti = g / G;
+                    const int idx = ct + (k0 + k) * AT, g = sg.rt * MT + idx / CH, ti = g / G;
                     v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (k0 + k < MT * CH / kAuxThreads && ti < rq.n)
+                    if (ti < sg.n)
                         v[k] = *reinterpret_cast<const uint4 *>(
-                            p.q + (rq.tok + ti) * p.ld_q + (long long)(walk.h * G + g - ti * G) * D + 8 * (idx % CH));
+                            p.q + (sg.tok + ti) * p.ld_q + (long long)(sg.h * G + g - ti * G) * D + 8 * (idx % CH));
                 }
-                if (!waited && seg > 0)
-                    bar_wait(bQFree, (seg - 1) & 1, ok); // the last segment's scores are done
-                waited = true;
+                if (k0 == 0)
+                    bar_wait(bQFree, free_ph, ok); // the last segment's scores are done
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * kAuxThreads, qr = idx / CH, c = idx % CH;
-                    if (k0 + k >= MT * CH / kAuxThreads)
-                        break;
-                    uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
+                    const int idx = ct + (k0 + k) * AT, qr = idx / CH, c = idx % CH;
+                    const uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
                     if constexpr (C::F8) {
-                        float mx = 0.0f;
+                        float f[8], mx = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                        for (int e = 0; e < 4; ++e) {
+                            f[2 * e] = __uint_as_float(w[e] << 16);
+                            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                            mx = fmaxf(mx, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                        }
 #pragma unroll
                         for (int o = CH / 2; o; o >>= 1)
                             mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
                         // both the power and its inverse are normal fp32 numbers
                         const int up = min(max(7 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
                         const float mul = pow2f(up);
+                        uint32_t part[2][2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<true>(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 x = make_float2(f[2 * e] * mul, f[2 * e + 1] * mul);
+                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t h2 = e4m3x2_to_f16x2(hi);
+                            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                            part[0][e >> 1] = e & 1 ? part[0][e >> 1] | hi << 16 : hi;
+                            part[1][e >> 1] = e & 1 ? part[1][e >> 1] | lo << 16 : lo;
+                        }
                         if (c == 0)
-                            s_f[seg & 3][qr] = pow2f(-up);
-                    }
+                            s_f[segs & 3][qr] = pow2f(-up);
 #pragma unroll
-                    for (int cp = 0; cp < C::COPIES; ++cp)
-                        *reinterpret_cast<uint4 *>(smem + op_off(qr + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int cp = 0; cp < C::COPIES; ++cp)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<uint2 *>(smem + e * C::SUB + op_off(qr + cp * MT, c >> 1) + 8 * (c & 1)) =
+                                    make_uint2(part[e][0], part[e][1]);
+                    } else {
+#pragma unroll
+                        for (int cp = 0; cp < C::COPIES; ++cp)
+                            *reinterpret_cast<uint4 *>(smem + op_off(qr + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
             }
+            free_ph ^= 1;
+            ++segs;
             fence_async_smem();
             __syncwarp();
             if (lane == 0)
                 bar_arrive(bQ);
-            ++seg;
 
-            const int nt = (walk.nu + 1) / 2, end = walk.key_end(), key0 = walk.j0 * kBN;
-            for (int t = 0; t < nt; ++t, ++i) {
-                const int kt = key0 + t * kTile;
+            for (int t = 0; t < sg.nt; ++t) {
+                const bool is_tail = t >= sg.first_tail;
+                uint8_t *vs; // the tile's values, 16 bits
                 if constexpr (C::F8) {
-#pragma unroll 1
-                    for (int n = 2 * i; n < 2 * i + 2; ++n) {
-                        const int rs = n % max(C::RS, 1), s = n % C::NS;
-                        bar_wait(bRFull + 8 * rs, (n / max(C::RS, 1)) & 1, ok);
-                        if (n >= C::NS)
-                            bar_wait(bEmpty + 8 * s, (n / C::NS - 1) & 1, ok);
-                        __syncwarp();
-                        const uint8_t *src = smem + (sRaw - sQ) + rs * C::RAW;
-                        uint8_t *dst = smem + (sKV - sQ) + s * C::SLOT;
-#pragma unroll 4
-                        for (int k = 0; k < kTile * D / 16 / kAuxThreads; ++k) {
-                            const int idx = ct + k * kAuxThreads, row = idx / (D / 16), c = idx % (D / 16);
-                            const int x = c ^ (((row * a.pitch) >> 7) & (D / 16 - 1)); // the copies' swizzle
-                            const uint4 v = *reinterpret_cast<const uint4 *>(src + row * a.pitch + 16 * x);
-                            *reinterpret_cast<uint4 *>(dst + op_off(row, 2 * c)) =
-                                make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
-                                           e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
-                            *reinterpret_cast<uint4 *>(dst + op_off(row, 2 * c + 1)) =
-                                make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
-                                           e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16));
-                        }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            bar_arrive(bFull + 8 * s);
-                            bar_arrive(bREmpty + 8 * rs);
-                        }
+                    bar_wait(bFull + 8 * vr.s, vr.ph, ok);
+                    bar_wait(bVEmpty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, ok);
+                    __syncwarp();
+                    const uint8_t *src = smem + (sKV - sQ) + vr.s * slot_bytes;
+                    vs = smem + (sV - sQ) + (i & 1) * C::SLOT;
+                    constexpr int M = kTile * D / 16 / AT;
+                    uint4 v[M];
+#pragma unroll
+                    for (int k = 0; k < M; ++k) {
+                        const int idx = ct + k * AT, row = idx / (D / 16), c = idx % (D / 16);
+                        // the copies' swizzle: of 128 bytes, or of 64 with rows of 64
+                        const int x = c ^ (a.pitch == 128 ? row & 7 : (row >> 1) & 3);
+                        v[k] = *reinterpret_cast<const uint4 *>(src + row * a.pitch + 16 * x);
                     }
-                }
-                if (kt + kTile <= min(rq.len, end))
-                    continue;
-                // A tail tile: values behind the end become zero, and of the
-                // drafted tokens' those that are not finite are marked.
-                const int n = 2 * i + 1, sl = n % C::NS;
-                bar_wait(bFull + 8 * sl, (n / C::NS) & 1, ok);
-                __syncwarp();
-                uint8_t *vs = smem + (sKV - sQ) + sl * C::SLOT;
-#pragma unroll 1
-                for (int b = 0; b < 2; ++b) {
-                    const int vr = ct + 64 * b;
-                    bool odd = false;
-                    if (kt + vr >= end) {
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4 *>(vs + op_off(vr, c)) = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (kt + vr >= rq.len) {
-                        constexpr uint32_t EXP = C::F8 ? 0x7c007c00u : 0x7f807f80u;
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(vs + op_off(vr, c));
-                            odd |= (__vcmpeq2(v.x & EXP, EXP) | __vcmpeq2(v.y & EXP, EXP) | __vcmpeq2(v.z & EXP, EXP) |
-                                    __vcmpeq2(v.w & EXP, EXP)) != 0;
-                        }
+                    for (int k = 0; k < M; ++k) {
+                        const int idx = ct + k * AT, row = idx / (D / 16), c = idx % (D / 16);
+                        *reinterpret_cast<uint4 *>(vs + op_off(row, 2 * c)) =
+                            make_uint4(e4m3x2_to_f16x2(v[k].x & 0xffffu), e4m3x2_to_f16x2(v[k].x >> 16),
+                                       e4m3x2_to_f16x2(v[k].y & 0xffffu), e4m3x2_to_f16x2(v[k].y >> 16));
+                        *reinterpret_cast<uint4 *>(vs + op_off(row, 2 * c + 1)) =
+                            make_uint4(e4m3x2_to_f16x2(v[k].z & 0xffffu), e4m3x2_to_f16x2(v[k].z >> 16),
+                                       e4m3x2_to_f16x2(v[k].w & 0xffffu), e4m3x2_to_f16x2(v[k].w >> 16));
                     }
                     __syncwarp();
-                    const uint32_t ob = __ballot_sync(~0u, odd);
                     if (lane == 0)
-                        s_odd[tail & 3][vr >> 5] = ob;
+                        bar_arrive(bEmpty + 8 * vr.s);
+                    vr.step(2, slots);
+                    if (is_tail)
+                        named_sync<AT>(4); // the rows below are other warps' too
+                } else {
+                    bar_wait(bFull + 8 * vr.s, vr.ph, ok); // the keys, passed on
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(bEmpty + 8 * vr.s);
+                    vr.step(1, slots);
+                    bar_wait(bFull + 8 * vr.s, vr.ph, ok);
+                    __syncwarp();
+                    vs = smem + (sKV - sQ) + vr.s * slot_bytes;
                 }
-                fence_async_smem();
+                if (is_tail) {
+                    // A tail tile: values behind the end become zero, and of the
+                    // drafted tokens' those that are not finite are marked.
+                    const int kt = sg.key0 + t * kTile;
+                    uint32_t *odd_keys = s_odd[(sg.tail_index + t - sg.first_tail) % kRing];
+#pragma unroll 1
+                    for (int vrow = ct; vrow < kTile; vrow += AT) {
+                        bool odd = false;
+                        if (kt + vrow >= sg.end) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                *reinterpret_cast<uint4 *>(vs + op_off(vrow, c)) = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (kt + vrow >= sg.len) {
+                            constexpr uint32_t EXP = C::F8 ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(vs + op_off(vrow, c));
+                                odd |= (__vcmpeq2(v.x & EXP, EXP) | __vcmpeq2(v.y & EXP, EXP) | __vcmpeq2(v.z & EXP, EXP) |
+                                        __vcmpeq2(v.w & EXP, EXP)) != 0;
+                            }
+                        }
+                        __syncwarp();
+                        const uint32_t ob = __ballot_sync(~0u, odd);
+                        if (lane == 0)
+                            odd_keys[vrow >> 5] = ob;
+                    }
+                }
+                if (C::F8 || is_tail)
+                    fence_async_smem();
                 __syncwarp();
-                if (lane == 0)
-                    bar_arrive(bTail + 8 * (tail & 3));
-                ++tail;
+                if (lane == 0) {
+                    bar_arrive(C::F8 ? bVFull + 8 * (i & 1) : bEmpty + 8 * vr.s);
+                    if (is_tail)
+                        bar_arrive(bTail + 8 * ((sg.tail_index + t - sg.first_tail) % kRing));
+                }
+                if (!C::F8)
+                    vr.step(1, slots);
+                ++i;
             }
         }
     } else {
         // ---- the softmax -------------------------------------------------
-        const int quad = warp / (MT / 32), row = (warp % (MT / 32)) * 32 + lane; // copy, row of the tile
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const uint32_t tO = tmem + kColO + lanes;
-        Split split{};
-        int i = 0, seg = 0, tail = 0;
-        while (walk.next(p, G, MT)) {
-            const Request &rq = walk.rq;
-            const int nt = (walk.nu + 1) / 2, end = walk.key_end(), key0 = walk.j0 * kBN;
-            const int g = walk.rt * MT + row, ti = g / G;
-            const bool live = ti < rq.n;
+        const int grp = warp >> 2, wq = warp & 3;
+        const int quad = wq / (MT / 32), row = (wq % (MT / 32)) * 32 + lane; // copy, row of the tile
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const uint32_t tS = tmem + grp * kTile + lanes, tO = tmem + kColO + grp * 128 + lanes;
+        const int gtid = tid & (kGroup - 1);
+        Ring seg{0, 0};
+        uint32_t s_ph = 0; // of this group's next tile: S, P, O take the same turns
+        int i0 = 0, segs = 0;
+        for (;;) {
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            __syncwarp();
+            const Seg sg = s_seg[seg.s];
+            if (!led || sg.nt == 0)
+                break;
+            const bool both = sg.nt > 1, takes = both || (i0 & 1) == grp;
+            const int g = sg.rt * MT + row, ti = g / G;
+            const bool live = ti < sg.n;
             const int tok_i = live ? ti : 0;
             const bool warp_live = __any_sync(~0u, live);
-            const uint64_t first = key0 + nt * kTile > rq.len ? tree_bits(p, rq, tok_i) : 0;
+            Request rq;
+            rq.tok = sg.tok;
+            rq.n = sg.n;
+            rq.len = sg.len;
+            const uint64_t first = takes && sg.first_tail < sg.nt ? tree_bits(p, rq, tok_i) : 0;
             const float base_factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
             float factor = fmaxf(base_factor, 1e-37f); // a scale of zero: all scores alike
             float m = -INFINITY, l = 0.0f;             // reference (base 2), sum
+            const int t0 = (grp ^ i0) & 1;
 
-            for (int t = 0; t < nt; ++t, ++i) {
-                const uint32_t tS = tmem + (i & 1) * kTile + lanes;
-                const int kt = key0 + t * kTile, kq = kt + quad * C::KW; // first key of the tile, of this copy
-                bar_wait(bS + 8 * (i & 1), (i >> 1) & 1, ok);
-                if (i >= 2)
-                    bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, ok);
+            for (int t = t0; t < sg.nt; t += 2) {
+                const int kt = sg.key0 + t * kTile;
+                bar_wait(bS + 8 * grp, s_ph, ok);
                 __syncwarp();
                 tc_after();
-                if (tid == 0)
-                    s_acc[i & 1] = 0;
+                if (gtid == 0)
+                    s_acc[grp] = 0;
                 if constexpr (C::F8)
-                    if (t == 0)
-                        factor = fmaxf(base_factor * s_f[seg & 3][row], 1e-37f);
-                uint32_t s[C::KW];
-                if (warp_live) {
-#pragma unroll
-                    for (int c = 0; c < C::KW; c += 32)
-                        tmem_ld32(tS + quad * C::KW + c, s + c);
-#pragma unroll
-                    for (int c = 0; c < C::KW; c += 32)
-                        tmem_ld_wait(s + c);
-                }
+                    if (t == t0)
+                        factor = fmaxf(base_factor * s_f[segs & 3][row], 1e-37f);
                 // Tiles that reach the drafted tokens or the end, or hold a key
                 // without a page.
-                const uint32_t *bad = s_bad[i & 7];
-                const bool is_tail = kt + kTile > min(rq.len, end);
-                uint64_t vis[(C::KW + 63) / 64];
-                if (is_tail || (bad[0] | bad[1] | bad[2] | bad[3])) {
+                const uint32_t *bad = s_bad[(i0 + t) % kTiles];
+                const bool is_tail = t >= sg.first_tail;
+                const bool masked = is_tail || (bad[0] | bad[1] | bad[2] | bad[3]);
+                uint32_t vis[C::NCH];
+                if (masked) {
 #pragma unroll
-                    for (int c = 0; c < C::KW; c += 64) {
-                        const int w = (quad * C::KW + c) >> 5;
-                        const uint64_t b = C::KW >= 64 ? bad[w] | ((uint64_t)bad[w + 1] << 32) : bad[w];
-                        vis[c / 64] = visible(p, rq, tok_i, first, kq + c, end) & ~b;
+                    for (int c = 0; c < C::NCH; c += 2) {
+                        const int ch = quad * C::NCH + c;
+                        const uint64_t v = visible(p, rq, tok_i, first, kt + 32 * ch, sg.end);
+                        vis[c] = (uint32_t)v & ~bad[ch];
+                        if (C::NCH > 1)
+                            vis[c + (C::NCH > 1)] = (uint32_t)(v >> 32) & ~bad[ch + 1];
                     }
-#pragma unroll
-                    for (int c = 0; c < C::KW; ++c)
-                        if (!((vis[c / 64] >> (c & 63)) & 1))
-                            s[c] = 0xff800000u;
                 }
                 if (warp_live) {
-                    float mx = -INFINITY;
+                    uint32_t s[32];
+                    auto chunk = [&](int c) { // of this copy's: scores, unseen keys' at -infinity
+                        tmem_ld32(tS + 32 * (quad * C::NCH + c), s);
+                        tmem_ld_wait(s);
+                        if (masked)
 #pragma unroll
-                    for (int c = 0; c < C::KW; ++c)
-                        mx = fmaxf(mx, __uint_as_float(s[c]));
-                    mx *= factor;
+                            for (int e = 0; e < 32; ++e)
+                                if (!((vis[c] >> e) & 1))
+                                    s[e] = 0xff800000u;
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < C::NCH; ++c) {
+                        chunk(c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor;
                     // the reference moves for the first keys seen, and when outgrown
-                    const bool grow = mx > m + kGrowth;
+                    const bool grow = top > m + kGrowth;
                     if (__any_sync(~0u, grow)) {
-                        const float to = grow ? mx : m;
-                        const float corr = grow ? exp2_fast(m - to) : 1.0f;
-                        m = to;
+                        const float corr = grow ? exp2_fast(m - top) : 1.0f;
+                        m = grow ? top : m;
                         l *= corr;
-                        if (t > 0) {
-                            bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, ok);
-                            __syncwarp();
-                            tc_after();
+                        if (t >= 2) { // this group's last product is done: S was issued after it
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + c, o);
-                                tmem_ld_wait(o);
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + c, o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                                tmem_st32(tO + c, o);
+                                tmem_st16(tO + c, o);
                             }
                         }
                     }
@@ -595,198 +759,233 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // The weights are rounded to the values' type for the product
                     // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
                     // small ones, 2^-25); their sum l is of the unrounded ones.
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    uint32_t w[C::KW / 2];
+                    float2 sum[2] = {};
 #pragma unroll
-                    for (int c = 0; c < C::KW; c += 2) {
-                        const float x = exp2_fast(fmaf(__uint_as_float(s[c]), factor, -ref));
-                        const float y = exp2_fast(fmaf(__uint_as_float(s[c + 1]), factor, -ref));
-                        sum[c & 2] += x;
-                        sum[(c & 2) + 1] += y;
-                        w[c / 2] = pack2<C::F8>(x, y);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    if constexpr (C::COPIES == 1) {
-                        tmem_st32(tS, w);
-                        tmem_st32(tS + 32, w + 32);
-                    } else {
-                        const uint32_t z[32] = {};
+                    for (int c = 0; c < C::NCH; ++c) {
+                        if (C::NCH > 1)
+                            chunk(c);
+                        uint32_t w[16];
 #pragma unroll
-                        for (int b = 0; b < C::COPIES; ++b) {
-                            if constexpr (MT == 64)
-                                tmem_st32(tS + 32 * b, b == quad ? w : z);
-                            else
-                                tmem_st16(tS + 16 * b, b == quad ? w : z);
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 x = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                             make_float2(factor, factor), make_float2(-ref, -ref));
+                            x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+                            w[e / 2] = pack2<C::F8>(x.x, x.y);
                         }
+                        tmem_st16(tS + 16 * (quad * C::NCH + c), w); // over scores already read
+                    }
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                    if constexpr (C::COPIES > 1) {
+                        const uint32_t z[16] = {};
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b / C::NCH != quad)
+                                tmem_st16(tS + 16 * b, z);
                     }
                     tmem_st_wait();
                 }
                 if (is_tail) {
-                    bar_wait(bTail + 8 * (tail & 3), (tail >> 2) & 1, ok);
-                    const uint32_t *odd = s_odd[tail & 3];
-                    ++tail;
+                    const int tail = sg.tail_index + t - sg.first_tail;
+                    bar_wait(bTail + 8 * (tail % kRing), (tail / kRing) & 1, ok);
+                    const uint32_t *odd = s_odd[tail % kRing];
                     if (odd[0] | odd[1] | odd[2] | odd[3]) {
                         // Rare: what is not finite must not reach, times zero, the
                         // rows that do not see its key. It is added to O here, for
                         // the rows that do, and taken out of the slot.
-                        const int n = 2 * i + 1, sl = n % C::NS;
-                        uint8_t *vs = smem + (sKV - sQ) + sl * C::SLOT;
-                        if (t > 0)
-                            bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, ok);
+                        uint8_t *vs;
+                        if constexpr (C::F8)
+                            vs = smem + (sV - sQ) + grp * C::SLOT;
+                        else
+                            vs = smem + (sKV - sQ) + (2 * (i0 + t) + 1) % slots * slot_bytes;
                         __syncwarp();
-                        tc_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + c, o);
-                            tmem_ld_wait(o);
-                            if (t == 0)
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c, o);
+                            if (t < 2)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = 0u;
 #pragma unroll 1
-                            for (int k = 0; k < C::KW; ++k) {
-                                const int kr = quad * C::KW + k; // row of the slot
-                                if (!((odd[kr >> 5] >> (kr & 31)) & 1) || !((vis[k >> 6] >> (k & 63)) & 1))
+                            for (int k = 0; k < 32 * C::NCH; ++k) {
+                                const int kr = quad * 32 * C::NCH + k; // row of the slot
+                                uint32_t v = vis[0];
+#pragma unroll
+                                for (int x = 1; x < C::NCH; ++x)
+                                    v = k >> 5 == x ? vis[x] : v;
+                                if (!((odd[kr >> 5] >> (kr & 31)) & 1) || !((v >> (k & 31)) & 1))
                                     continue;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
+                                for (int e = 0; e < 16; ++e) {
                                     const uint16_t b = *reinterpret_cast<const uint16_t *>(vs + op_off(kr, (c + e) >> 3) + 2 * (e & 7));
-                                    const float v = C::F8 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
-                                    if (!isfinite(v))
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+                                    const float x = C::F8 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
+                                    if (!isfinite(x))
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
                                 }
                             }
                             __syncwarp();
-                            tmem_st32(tO + c, o);
+                            tmem_st16(tO + c, o);
                         }
                         tmem_st_wait();
-                        soft_sync();
-                        if ((odd[warp] >> lane) & 1) {
+                        named_sync<kGroup>(2 + grp);
+                        if ((odd[wq] >> lane) & 1) {
                             constexpr uint16_t EXP = C::F8 ? 0x7c00 : 0x7f80;
                             for (int e = 0; e < D; ++e) {
-                                uint16_t *b = reinterpret_cast<uint16_t *>(vs + op_off(tid, e >> 3) + 2 * (e & 7));
+                                uint16_t *b = reinterpret_cast<uint16_t *>(vs + op_off(gtid, e >> 3) + 2 * (e & 7));
                                 if ((*b & EXP) == EXP)
                                     *b = 0;
                             }
                         }
-                        if (tid == 0)
-                            s_acc[i & 1] = t == 0;
+                        if (gtid == 0)
+                            s_acc[grp] = t < 2;
                         fence_async_smem();
-                        soft_sync();
+                        named_sync<kGroup>(2 + grp);
                     }
                 }
                 tc_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(bP + 8 * (i & 1));
+                    bar_arrive(bP + 8 * grp);
+                s_ph ^= 1;
             }
-            ++seg;
 
-            // ---- the segment's end: O is complete ----
-            const int last = i - 1;
-            const bool whole = walk.whole();
-            const int which = walk.j0 == 0 ? 1 : 0;
-            float *part = part_of(p, blockIdx.x, which, MT, D);
-            if (which && !whole) {
-                split.parts = cta_of(U, walk.item0 + rq.tiles - 1, ctas) - (int)blockIdx.x + 1;
-                split.tok = rq.tok;
-                split.n = rq.n;
-                split.h = walk.h;
-                split.rt = walk.rt;
-            }
-            const long long tk = rq.tok + tok_i;
-            const int hq = walk.h * G + g - ti * G;
-            if (last >= 1)
-                bar_wait(bO + 8 * ((last - 1) & 1), ((last - 1) >> 1) & 1, ok);
-            bar_wait(bO + 8 * (last & 1), (last >> 1) & 1, ok);
-            __syncwarp();
-            tc_after();
-            float f = 1.0f, top = m, sum = l;
-            if constexpr (C::COPIES > 1) {
-                s_m[quad][row] = m;
-                s_l[quad][row] = l;
-                soft_sync();
-                top = s_m[0][row];
-#pragma unroll
-                for (int c = 1; c < C::COPIES; ++c)
-                    top = fmaxf(top, s_m[c][row]);
-                sum = 0.0f; // a copy that saw nothing has l = 0 (or NaN)
-#pragma unroll
-                for (int c = 0; c < C::COPIES; ++c)
-                    sum += s_m[c][row] == -INFINITY ? s_l[c][row] : s_l[c][row] * exp2_fast(s_m[c][row] - top);
-                f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
-            }
-            const float inv = sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
-            if (live && quad == 0) {
-                if (!whole) {
-                    part[MT * D + row] = top;
-                    part[MT * D + MT + row] = sum;
-                } else if (p.lse) {
-                    p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
-                }
-            }
-            uint16_t *orow = p.out + tk * p.ld_out + (long long)hq * D;
-            float *prow = part + (size_t)row * D;
-            constexpr int CW = 32 / C::COPIES; // columns of each 32 that this thread writes
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                float o[CW];
-                if (warp_live) {
-                    uint32_t raw[32];
-                    tmem_ld32(tO + c0, raw);
-                    tmem_ld_wait(raw);
-                    if constexpr (C::COPIES == 1) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __uint_as_float(raw[e]);
-                    } else {
-                        float4 *buf = reinterpret_cast<float4 *>(smem + (sJoin - sQ)) + (quad * MT + row) * 8;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            buf[e ^ (row & 7)] = make_float4(__uint_as_float(raw[4 * e]) * f, __uint_as_float(raw[4 * e + 1]) * f,
-                                                             __uint_as_float(raw[4 * e + 2]) * f, __uint_as_float(raw[4 * e + 3]) * f);
-                    }
-                }
-                if constexpr (C::COPIES > 1) {
-                    soft_sync();
-                    const float4 *buf = reinterpret_cast<const float4 *>(smem + (sJoin - sQ)) + row * 8;
-#pragma unroll
-                    for (int e = 0; e < CW / 4; ++e) {
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int c = 0; c < C::COPIES; ++c) {
-                            const float4 y = buf[c * MT * 8 + ((quad * (CW / 4) + e) ^ (row & 7))];
-                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                        }
-                        o[4 * e] = x.x;
-                        o[4 * e + 1] = x.y;
-                        o[4 * e + 2] = x.z;
-                        o[4 * e + 3] = x.w;
-                    }
-                    soft_sync();
-                }
-                if (live) {
-                    if (whole) {
-#pragma unroll
-                        for (int e = 0; e < CW; e += 8)
-                            *reinterpret_cast<uint4 *>(orow + c0 + quad * CW + e) =
-                                make_uint4(pack2<false>(o[e] * inv, o[e + 1] * inv), pack2<false>(o[e + 2] * inv, o[e + 3] * inv),
-                                           pack2<false>(o[e + 4] * inv, o[e + 5] * inv), pack2<false>(o[e + 6] * inv, o[e + 7] * inv));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < CW; e += 4)
-                            *reinterpret_cast<float4 *>(prow + c0 + quad * CW + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
-                }
+            // ---- the segment's end -----------------------------------------------
+            if (takes) {
+                bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
                 __syncwarp();
+                tc_after();
+                const long long tk = sg.tok + tok_i;
+                const int hq = sg.h * G + g - ti * G;
+                float *part = part_of(p, blockIdx.x, sg.which, MT, D);
+                uint16_t *orow = p.out + tk * p.ld_out + (long long)hq * D;
+                float *prow = part + (size_t)row * D;
+                auto put_sums = [&](float top, float sum) {
+                    if (!sg.whole) {
+                        part[MT * D + row] = top;
+                        part[MT * D + MT + row] = sum;
+                    } else if (p.lse) {
+                        p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    }
+                };
+                // Joins the NSRC sources of a row, 16 columns at a time through
+                // shared memory, each thread writing CW columns of its row.
+                auto finish = [&](auto nsrc) {
+                    constexpr int NSRC = decltype(nsrc)::value, CW = 16 / NSRC;
+                    constexpr bool BOTH = NSRC == 2 * C::COPIES;
+                    const int src = BOTH ? grp * C::COPIES + quad : quad;
+                    auto sync = [&] {
+                        if constexpr (BOTH)
+                            named_sync<2 * kGroup>(1);
+                        else
+                            named_sync<kGroup>(2 + grp);
+                    };
+                    const int base = BOTH ? 0 : grp * C::COPIES; // first source's entries
+                    float4 *buf = reinterpret_cast<float4 *>(smem + (sJoin - sQ)) + base * MT * 4;
+                    s_m[base + src][row] = m;
+                    s_l[base + src][row] = l;
+                    sync();
+                    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < NSRC; ++c)
+                        top = fmaxf(top, s_m[base + c][row]);
+#pragma unroll
+                    for (int c = 0; c < NSRC; ++c) { // one that saw nothing has l = 0 (or NaN)
+                        const float mc = s_m[base + c][row], lc = s_l[base + c][row];
+                        sum += mc == -INFINITY ? lc : lc * exp2_fast(mc - top);
+                    }
+                    const float f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
+                    const float inv = sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
+                    if (live && src == 0)
+                        put_sums(top, sum);
+                    const int sw = (row >> 1) & 3;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        if (warp_live) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c0, o);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                buf[(src * MT + row) * 4 + (e ^ sw)] =
+                                    make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                        }
+                        sync();
+                        if (live) {
+                            float x[CW] = {};
+                            const int col = src * CW;
+#pragma unroll
+                            for (int c = 0; c < NSRC; ++c) {
+                                const float *b = reinterpret_cast<const float *>(buf + (c * MT + row) * 4);
+                                if constexpr (CW == 2) {
+                                    const float2 y = *reinterpret_cast<const float2 *>(b + (((col >> 2) ^ sw) << 2) + (col & 3));
+                                    x[0] += y.x;
+                                    x[1] += y.y;
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < CW; e += 4) {
+                                        const float4 y = *reinterpret_cast<const float4 *>(b + ((((col + e) >> 2) ^ sw) << 2));
+                                        x[e] += y.x;
+                                        x[e + 1] += y.y;
+                                        x[e + 2] += y.z;
+                                        x[e + 3] += y.w;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < CW; e += 2) {
+                                if (sg.whole)
+                                    *reinterpret_cast<uint32_t *>(orow + c0 + col + e) = pack2<false>(x[e] * inv, x[e + 1] * inv);
+                                else
+                                    *reinterpret_cast<float2 *>(prow + c0 + col + e) = make_float2(x[e], x[e + 1]);
+                            }
+                        }
+                        sync();
+                    }
+                };
+                if (both) {
+                    finish(std::integral_constant<int, 2 * C::COPIES>{});
+                } else if constexpr (C::COPIES > 1) {
+                    finish(std::integral_constant<int, C::COPIES>{});
+                } else {
+                    const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
+                    if (live)
+                        put_sums(m, l);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
+                        if (live && sg.whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(orow + c);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t b[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    b[x] = pack2<false>(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                                dst[e] = make_uint4(b[0], b[1], b[2], b[3]);
+                            }
+                        } else if (live) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(prow + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                tc_before();
             }
-            tc_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(bSegFree + 8 * seg.s);
+            seg.step(1, kRing);
+            i0 += sg.nt;
+            ++segs;
         }
-        if (tid == 0)
-            static_cast<Split *>(p.workspace)[blockIdx.x] = split;
     }
-    if (!ok)
+    if (!ok || !led)
         set_status(p.status, SGQ_STATUS_TIMEOUT);
     tc_before();
     __syncthreads();
@@ -794,55 +993,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-// Joins the parts of the item that CTA blockIdx.x of the attention started and
-// did not finish, in key order: one warp per row, kJoinRows rows a CTA.
-constexpr int kJoinRows = 8;
+// Joins the parts of the items that several CTAs worked on, in key order. The
+// CTAs of an item share its rows here too: CTA c0 + x takes rows x, x + parts,
+// ... A row is read by as many of the CTA's warps as there are rows too few.
+constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const AttnProblem p, int MT)
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem p, int MT)
 {
-    constexpr int LPR = D / 4; // lanes per row: with D = 64 two parts are read side by side
-    constexpr int SIDE = 32 / LPR;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    constexpr int LPR = D / 4;     // lanes per row: with D = 64 two parts are read side by side
+    constexpr int SIDE = 32 / LPR, BATCH = 4;
+    __shared__ float4 s_o[kJoinWarps][LPR];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = lane % LPR;
     grid_launch_dependents();
     grid_dependency_wait();
     const Split sp = static_cast<const Split *>(p.workspace)[blockIdx.x];
-    const int G = p.Hq / p.cache.heads, g = sp.rt * MT + row, ti = g / G;
-    if (sp.parts == 0 || ti >= sp.n)
+    if (sp.parts == 0)
         return;
-    const int x = lane % LPR;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-    for (int k = lane / LPR; k < sp.parts; k += SIDE) {
-        const float *part = part_of(p, blockIdx.x + k, k == 0, MT, D);
-        const float pm = part[MT * D + row], pl = part[MT * D + MT + row];
-        const float4 v = *reinterpret_cast<const float4 *>(part + (size_t)row * D + 4 * x);
-        const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.0f : top;
-        const float a = exp2_fast(m - ref), b = exp2_fast(pm - ref);
-        o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
-        l = l * a + pl * b;
-        m = top;
+    const int G = p.Hq / p.cache.heads, first = (int)(blockIdx.x >> 1) - sp.c0;
+    const int rows = min((long long)MT, (long long)sp.n * G - (long long)sp.rt * MT);
+    const int mine = rows > first ? (rows - first + sp.parts - 1) / sp.parts : 0;
+    int wpr = kJoinWarps; // warps per row
+    while (wpr > 1 && wpr * mine > kJoinWarps)
+        wpr >>= 1;
+    for (int k0 = 0; k0 < mine; k0 += kJoinWarps / wpr) {
+        const int k = k0 + warp / wpr, row = first + k * sp.parts;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.0f;
+        if (k < mine) {
+            const int step = SIDE * wpr;
+            for (int b = (warp % wpr) * SIDE + lane / LPR; b < sp.parts; b += BATCH * step) {
+                float pm[BATCH], pl[BATCH];
+                float4 v[BATCH];
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e) {
+                    const int c = b + e * step;
+                    const float *part = part_of(p, sp.c0 + c, c == 0, MT, D);
+                    const bool in = c < sp.parts;
+                    pm[e] = in ? part[MT * D + row] : -INFINITY;
+                    pl[e] = in ? part[MT * D + MT + row] : 0.0f;
+                    v[e] = in ? *reinterpret_cast<const float4 *>(part + (size_t)row * D + 4 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                float top = m;
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e)
+                    top = fmaxf(top, pm[e]);
+                const float ref = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - ref);
+                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                l *= f;
+                m = top;
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e) {
+                    const float w = exp2_fast(pm[e] - ref);
+                    o = make_float4(o.x + v[e].x * w, o.y + v[e].y * w, o.z + v[e].z * w, o.w + v[e].w * w);
+                    l += pl[e] * w;
+                }
+            }
+        }
+        if constexpr (SIDE == 2) {
+            const float m2 = __shfl_xor_sync(~0u, m, 16), l2 = __shfl_xor_sync(~0u, l, 16);
+            const float4 v = make_float4(__shfl_xor_sync(~0u, o.x, 16), __shfl_xor_sync(~0u, o.y, 16),
+                                         __shfl_xor_sync(~0u, o.z, 16), __shfl_xor_sync(~0u, o.w, 16));
+            const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+            const float f = exp2_fast(m - ref), w = exp2_fast(m2 - ref);
+            o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+            l = l * f + l2 * w;
+            m = top;
+        }
+        if (wpr > 1) {
+            if (lane < LPR)
+                s_o[warp][x] = o;
+            if (lane == 0) {
+                s_m[warp] = m;
+                s_l[warp] = l;
+            }
+            __syncthreads();
+            if (warp % wpr == 0) {
+                for (int w = warp + 1; w < warp + wpr; ++w) {
+                    const float m2 = s_m[w], top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+                    const float f = exp2_fast(m - ref), e = exp2_fast(m2 - ref);
+                    const float4 v = s_o[w][x];
+                    o = make_float4(o.x * f + v.x * e, o.y * f + v.y * e, o.z * f + v.z * e, o.w * f + v.w * e);
+                    l = l * f + s_l[w] * e;
+                    m = top;
+                }
+            }
+            __syncthreads();
+        }
+        if (k < mine && warp % wpr == 0 && lane < LPR) {
+            const int g = sp.rt * MT + row, ti = g / G, hq = sp.h * G + g - ti * G;
+            const long long t = sp.tok + ti;
+            const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
+            *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + 4 * x) =
+                make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+            if (p.lse && x == 0)
+                p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
     }
-    if constexpr (SIDE == 2) {
-        const float m2 = __shfl_xor_sync(~0u, m, 16), l2 = __shfl_xor_sync(~0u, l, 16);
-        const float4 v = make_float4(__shfl_xor_sync(~0u, o.x, 16), __shfl_xor_sync(~0u, o.y, 16),
-                                     __shfl_xor_sync(~0u, o.z, 16), __shfl_xor_sync(~0u, o.w, 16));
-        const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
-        const float a = exp2_fast(m - ref), b = exp2_fast(m2 - ref);
-        o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
-        l = l * a + l2 * b;
-        m = top;
-    }
-    if (lane >= LPR)
-        return;
-    const long long t = sp.tok + ti;
-    const int hq = sp.h * G + g - ti * G;
-    const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
-    *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + 4 * x) =
-        make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
-    if (p.lse && x == 0)
-        p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -866,7 +1114,7 @@ EncodeTiled encoder()
 // (element, slot, head, page) of the cache; a box is 128 bytes of a row (64
 // where the row has no more) times `box` slots of one page and head. A
 // dimension of one entry has no stride of its own: any valid one will do.
-bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box)
+bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box, int pitch)
 {
     const bool f8 = c.type == SGQ_TYPE_E4M3;
     const int es = f8 ? 1 : 2, inner = std::min(c.dim, 128 / es);
@@ -878,7 +1126,7 @@ bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box)
     const cuuint32_t boxes[4] = {(cuuint32_t)inner, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
     return encoder()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes,
                      ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     pitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -891,16 +1139,16 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
     a.box = 1;
     while (a.box < 64 && p.cache.page % (2 * a.box) == 0)
         a.box *= 2;
-    a.pitch = a.box == 1 ? 128 : D;
+    a.pitch = C::F8 && a.box > 1 ? D : 128;
     CUtensorMap kmap, vmap;
     if (!encoder())
         return cudaErrorNotSupported;
-    if (!encode(&kmap, p.cache, p.cache.k, a.box) || !encode(&vmap, p.cache, p.cache.v, a.box))
+    if (!encode(&kmap, p.cache, p.cache.k, a.box, a.pitch) || !encode(&vmap, p.cache, p.cache.v, a.box, a.pitch))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), kThreads, C::SMEM, 1, stream, a, kmap, vmap);
+    cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, a, kmap, vmap);
     if (e != cudaSuccess)
         return e;
-    return launch_step(join_kernel<D>, dim3(grid, MT / kJoinRows), 32 * kJoinRows, 0, 1, stream, p, MT);
+    return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);
 }
 
 template <int D, int KV>
@@ -922,7 +1170,7 @@ size_t attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D)
     (void)R;
     (void)Hq;
     (void)Hkv;
-    return kMaxGrid * sizeof(Split) + (size_t)2 * kMaxGrid * kMaxMT * (D + 2) * sizeof(float);
+    return 2 * kMaxGrid * sizeof(Split) + (size_t)2 * kMaxGrid * kMaxMT * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnProblem &p, int num_sms, cudaStream_t stream)

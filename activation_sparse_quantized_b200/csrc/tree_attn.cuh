@@ -56,17 +56,17 @@ __device__ __forceinline__ int cta_of(long long U, long long u, int C)
     return (int)(((u + 1) * C - 1) / U);
 }
 
-// An item that CTA c starts and others go on with, for the kernel that joins
-// its parts: those of CTAs c, c + 1, ..., c + parts - 1 (parts = 0: none).
+// A CTA's share of an item that several CTAs work on, c0 to c0 + parts - 1
+// (parts = 0: none): the one it goes on with ([0]) and the one it starts ([1]).
 struct __align__(32) Split {
-    int parts, tok, n, h, rt;
+    int parts, c0, tok, n, h, rt;
 };
 
-// The part that CTA c leaves of the item it starts (which = 1) or goes on with
-// (which = 0): MT rows of D sums, then the rows' references, then their sums.
+// The part that CTA c leaves of either: MT rows of D sums, then the rows'
+// references, then their sums.
 __device__ __forceinline__ float *part_of(const AttnProblem &p, int c, int which, int MT, int D)
 {
-    return reinterpret_cast<float *>(static_cast<char *>(p.workspace) + kMaxGrid * sizeof(Split)) +
+    return reinterpret_cast<float *>(static_cast<char *>(p.workspace) + 2 * kMaxGrid * sizeof(Split)) +
            (size_t)(2 * c + which) * (MT * (D + 2));
 }
 
@@ -139,7 +139,7 @@ __device__ __forceinline__ uint64_t visible(const AttnProblem &p, const Request 
 }
 
 // The segments of one CTA's run, in order: each is `nu` units, from unit j0 on,
-// of one item. Every warp that walks sees the same ones.
+// of one item.
 struct Walk {
     int r = 0, h = 0, rt = 0; // request, key head, row tile
     int j0 = 0, nu = 0;

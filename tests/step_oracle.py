@@ -86,9 +86,12 @@ def stored_tolerance(y, mag, dtype):
     return d + HALF_STEP[dtype] * (y.abs() + d) + LOWEST_STEP[dtype]
 
 
-def attention(q, lens, cu, keys, vals, sees, scale, k_scale=1.0, v_scale=1.0):
+def attention(q, lens, cu, keys, vals, sees, scale, k_scale=1.0, v_scale=1.0, eight=False):
     """keys, vals: per request [l + n, Hkv, D] fp64; sees: per request bool [n, l + n].
-    Returns (out, lse, weighted |v|, largest sum of |q_i k_i| scaled) in fp64, [T, Hq(, D)]."""
+    Returns (out, lse, weighted |v|, largest sum of |q_i k_i| scaled) in fp64, [T, Hq(, D)].
+    eight: q is taken in two 8-bit parts, each element off by at most 2^-17 of the
+    row's largest; that is added to the sums, as a multiple of what they stand for
+    in attention_tolerance ((D + 8) U of them)."""
     T, Hq, D = q.shape
     out = torch.zeros(T, Hq, D, dtype=torch.float64)
     mag = torch.zeros_like(out)
@@ -109,7 +112,10 @@ def attention(q, lens, cu, keys, vals, sees, scale, k_scale=1.0, v_scale=1.0):
                 out[t0 + i, h] = (w[:, None] * v).sum(0) * v_scale
                 mag[t0 + i, h] = (w[:, None] * v.abs()).sum(0) * v_scale
                 lse[t0 + i, h] = torch.logsumexp(s, 0)
-                dots[t0 + i, h] = ((k * x).abs().sum(-1) * abs(scale * k_scale)).max()
+                d = (k * x).abs().sum(-1)
+                if eight:
+                    d = d + k.abs().sum(-1) * x.abs().max() * (2.0 ** -17 / ((D + 8) * U))
+                dots[t0 + i, h] = (d * abs(scale * k_scale)).max()
     return out, lse, mag, dots
 
 

@@ -327,7 +327,7 @@ class AttnCase:
     def check(self, status=0):
         assert self.status.item() == status
         f8 = self.k.dtype == E4M3
-        out, lse, mag, dots = so.attention(self.q, self.lens, self.cu, self.keys, self.vals, self.sees, self.scale, self.ks, self.vs)
+        out, lse, mag, dots = so.attention(self.q, self.lens, self.cu, self.keys, self.vals, self.sees, self.scale, self.ks, self.vs, f8)
         n = self.cu[-1]
         got, gl = self.out.cpu().double(), self.lse.cpu().double()
         to, tl = so.attention_tolerance(out, lse, mag, dots, self.D, 2.0 ** -11 if f8 else 2.0 ** -8)
@@ -340,7 +340,8 @@ class AttnCase:
 
 @pytest.mark.parametrize("Hq,Hkv,D,page,layout,dtype", [
     (8, 8, 64, 16, "nhd", BF16), (8, 2, 128, 16, "hnd", BF16), (6, 2, 64, 24, "hnd", E4M3), (10, 2, 128, 7, "nhd", E4M3),
-    (16, 1, 128, 64, "nhd", BF16), (5, 1, 64, 1, "nhd", BF16), (7, 1, 128, 128, "hnd", E4M3)])
+    (16, 1, 128, 64, "nhd", BF16), (5, 1, 64, 1, "nhd", BF16), (7, 1, 128, 128, "hnd", E4M3),
+    (4, 2, 64, 5, "nhd", E4M3), (4, 1, 64, 2, "hnd", E4M3), (4, 4, 128, 12, "nhd", BF16)])
 @pytest.mark.parametrize("lens,news", [([0], [1]), ([1], [1]), ([63], [1]), ([64], [1]), ([127, 0, 65], [1, 3, 2]),
                                        ([300, 5, 64, 1000], [7, 16, 1, 33])])
 @pytest.mark.parametrize("tree", ["random", None])
@@ -391,7 +392,7 @@ def test_attention_rows_that_see_nothing_and_masked_values_that_are_not_finite()
             for r in range(2):
                 c.sees[r][3] = False
             got, lse = c.out.clone(), c.lse.clone()
-            ref, rl, mag, dots = so.attention(c.q, c.lens, c.cu, c.keys, c.vals, c.sees, c.scale, c.ks, c.vs)
+            ref, rl, mag, dots = so.attention(c.q, c.lens, c.cu, c.keys, c.vals, c.sees, c.scale, c.ks, c.vs, dtype == E4M3)
             to, tl = so.attention_tolerance(ref, rl, mag, dots, 128, 2.0 ** -8)
             rest = [t for t in range(c.T) if t not in own]
             assert ((got.cpu().double() - ref).abs() <= to)[rest].all()
@@ -663,7 +664,7 @@ def test_a_step_together(dtype):
             sees.append(see)
             b += news[r]
         ref, rl, mg, dots = so.attention(q[:T].cpu().view(T, Hq, D), lens, cu.tolist(), [torch.stack(z) for z in keys],
-                                         [torch.stack(z) for z in vals], sees, D ** -0.5, ks, vs)
+                                         [torch.stack(z) for z in vals], sees, D ** -0.5, ks, vs, dtype == E4M3)
         to, tl = so.attention_tolerance(ref, rl, mg, dots, D, 2.0 ** -11 if dtype == E4M3 else 2.0 ** -8)
         assert ((att[:T].cpu().double().view(T, Hq, D) - ref).abs() <= to).all() and ((lse[:T].cpu().double() - rl).abs() <= tl).all()
         r64, x64, tol, f = so.norm(o32.cpu(), w_post, None, 1.0, r0.cpu(), w_pre, 0.0, 1e-6)
