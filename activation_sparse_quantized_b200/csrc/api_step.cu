@@ -152,7 +152,7 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
 
 size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D)
 {
-    if (T < 1 || R < 1 || R > SGQ_MAX_REQUESTS || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
+    if (T < 1 || R < 1 || R > SGQ_MAX_REQUESTS || Hkv < 1 || Hq < Hkv || Hq > 32768 || Hq % Hkv != 0 ||
         (D != 64 && D != 128))
         return 0;
     return sgq::attn_workspace_bytes(T, R, Hq, Hkv, D);
@@ -170,9 +170,9 @@ int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int
     if (R < 1 || R > SGQ_MAX_REQUESTS)
         return SGQ_ERR_BATCH;
     const long long D = cache_host->dim, Hkv = cache_host->heads;
-    if (T < 1 || Hq < Hkv || Hq > 65536 || Hq % Hkv != 0 || table_ld < 1 ||
+    if (T < 1 || Hq < Hkv || Hq % Hkv != 0 || table_ld < 1 ||
         (long long)table_ld * cache_host->page > (1ll << 30) ||
-        (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))))
+        Hq > 32768 || (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))))
         return SGQ_ERR_SHAPE;
     if (!q || !lens || !cu_new || !table || !out || !workspace)
         return SGQ_ERR_NULL;

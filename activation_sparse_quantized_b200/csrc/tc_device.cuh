@@ -56,6 +56,18 @@ __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, bool &ok
     }
 }
 
+// Whether the phase of the given parity has completed.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done;
+}
+
 // Box (x, y, z, w) of a tensor map into shared memory, counted on bar.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             int z, int w, uint32_t bar)

@@ -26,19 +26,21 @@
 //  * one thread issues S = Q K^T (both from shared memory) into one of two
 //    accumulators, one tile ahead and across segments, and O += P V with P
 //    read from tensor memory, where it takes S's place;
-//  * two groups of four take the tiles in turn, one accumulator row per
-//    thread, turn S into P and have an O of their own, so that one group's
-//    exponentials overlap the other's. The reference for the exponent moves
-//    only when a row's maximum outgrows it by 2^8, so O is rescaled rarely. A
-//    segment of one tile is one group's alone;
-//  * the rest fetch the next segment's Q and look through the values next to
-//    the end. With 8-bit keys and values q is split into two 8-bit parts, so
-//    that S is a product of 8-bit operands as they lie, and these warps make
-//    the values fp16 (exact): weights of 8 bits would lose a long row's tail.
-// A tile of 32 or 64 rows (MT) is laid into the 128 several times, and copy c
-// takes part c of the keys, its P zero elsewhere: the copies' O are partial
-// sums over the keys, joined at the segment's end with the other group's. All
-// the softmax warps then share the exponentials of a few rows.
+//  * two groups of four turn S into P, one accumulator row per thread, and
+//    have an O of their own, so that one group's exponentials overlap the
+//    other's. The reference for the exponent moves only when a row's maximum
+//    outgrows it by 2^8, so O is rescaled rarely;
+//  * one or two fetch the next segment's Q, the rest look through the values
+//    next to the end. With 8-bit keys and values q is split into two 8-bit
+//    parts, so that S is a product of 8-bit operands as they lie, and the
+//    values are made fp16 (exact): weights of 8 bits would lose a long row's
+//    tail.
+// Row tiles (MT): with 256 rows each group has 128 of them and both see every
+// key. With fewer the groups take the tiles of keys in turn (a segment of one
+// tile is one group's alone), and 32 or 64 rows are laid into the 128 several
+// times: copy c takes part c of the keys, its P zero elsewhere, so that all the
+// softmax warps share the exponentials of a few rows. What the copies and
+// groups summed over their keys is joined at the segment's end.
 //
 // Every wait on a barrier is bounded by 0.2 s; one that runs out sets
 // SGQ_STATUS_TIMEOUT, the thread waits for no data any more and the kernel runs
@@ -58,7 +60,7 @@ namespace {
 
 constexpr int kTile = 128; // keys per product
 constexpr int kGroup = 128; // threads of a softmax group
-constexpr int kSoftWarps = 8, kProducer = 8, kIssuer = 9, kAux = 10; // warps
+constexpr int kSoftWarps = 8, kProducer = 8, kIssuer = 9, kQ = 10; // warps
 constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
@@ -68,16 +70,19 @@ constexpr unsigned long long kSegWaitNs = 2000000000ull;
 template <int D_, int KV, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_;
-    static constexpr bool F8 = KV == SGQ_TYPE_E4M3;
-    static constexpr int AUX = F8 ? 4 : 2, THREADS = 32 * (kAux + AUX);
-    static constexpr int COPIES = 128 / MT, NCH = 4 / COPIES; // copies of the rows, 32-key chunks of each
+    static constexpr bool F8 = KV == SGQ_TYPE_E4M3, TWO = MT == 256;
+    static constexpr int QW = F8 ? 2 : 1, VW = F8 ? 4 : 1;    // warps for Q, for the values
+    static constexpr int kV = kQ + QW, THREADS = 32 * (kV + VW);
+    static constexpr int ROWS = TWO ? 128 : MT;               // of a group
+    static constexpr int COPIES = 128 / ROWS, NCH = 4 / COPIES; // copies of the rows, 32-key chunks of each
     static constexpr int SUB = kTile * 128;                   // 128 rows x 128 bytes, swizzled
     static constexpr int NSUB = D / 64;
     static constexpr int SLOT = NSUB * SUB;                   // 128 keys (or values), 16 bits
-    static constexpr int KV_BYTES = F8 ? 96 * 1024 : D == 128 ? 5 * SLOT : 10 * SLOT; // the ring of copies
+    static constexpr int Q1 = F8 ? 2 * SUB : SLOT, Q = TWO ? 2 * Q1 : Q1; // 128 rows of q; all of them
+    static constexpr int KV_BYTES = F8 ? (TWO ? 64 : 96) * 1024 : (TWO ? 4 : 5) * (D == 128 ? 1 : 2) * SLOT; // the ring of copies
     static constexpr int MAX_SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
-    static constexpr int Q = F8 ? 2 * SUB : SLOT, JOIN = 2 * kGroup * 64;
+    static constexpr int JOIN = 2 * kGroup * 64;
     static constexpr int BARS = 2 * MAX_SLOTS + 2 * NV + 6 + 3 * kRing + 2;
     static constexpr int SMEM = 1024 + Q + KV_BYTES + NV * SLOT + JOIN + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
@@ -153,7 +158,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ int s_r;
     __shared__ Request s_rq;
     __shared__ Seg s_seg[kRing];
-    __shared__ float s_m[2 * C::COPIES][MT], s_l[2 * C::COPIES][MT];
+    __shared__ float s_m[2 * C::COPIES][C::ROWS], s_l[2 * C::COPIES][C::ROWS];
+    __shared__ long long s_row[2][C::ROWS]; // where a row's output goes, -1: nowhere
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
     __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
     __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
@@ -178,12 +184,12 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int s = 0; s < C::MAX_SLOTS; ++s) {
             bar_init(bFull + 8 * s, 1);
-            // read by the products and followed by the aux warps; 8-bit keys by the
-            // products alone, 8-bit values by the aux warps alone
-            bar_init(bEmpty + 8 * s, !C::F8 ? 1 + C::AUX : s & 1 ? C::AUX : 1);
+            // read by the products and followed by the value warps; 8-bit keys by the
+            // products alone, 8-bit values by the value warps alone
+            bar_init(bEmpty + 8 * s, !C::F8 ? 1 + C::VW : s & 1 ? C::VW : 1);
         }
         for (int s = 0; s < C::NV; ++s) {
-            bar_init(bVFull + 8 * s, C::AUX);
+            bar_init(bVFull + 8 * s, C::VW);
             bar_init(bVEmpty + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -193,11 +199,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             s_acc[b] = 0;
         }
         for (int b = 0; b < kRing; ++b) {
-            bar_init(bTail + 8 * b, C::AUX);
+            bar_init(bTail + 8 * b, C::VW);
             bar_init(bSeg + 8 * b, 1);
             bar_init(bSegFree + 8 * b, kSoftWarps);
         }
-        bar_init(bQ, C::AUX);
+        bar_init(bQ, C::QW);
         bar_init(bQFree, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -416,25 +422,31 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
             uint32_t q_ph = 0;
             int left = 0, nt = 0; // tiles of the segment without scores, all of them
-            // The scores of tile n, the next one; false when there is none.
-            auto scores = [&](int n) -> bool {
-                if (left == 0) {
+            bool ended = false;
+            // Whether there is a next tile; its segment is looked up.
+            auto next = [&]() -> bool {
+                if (left == 0 && !ended) {
                     bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
                     left = led ? *(volatile int *)&s_seg[seg.s].nt : 0;
-                    if (left == 0)
-                        return false;
-                    nt = left;
                     seg.step(1, kRing);
+                    ended = left == 0;
+                    nt = -left; // its Q has not been waited for
+                }
+                return !ended;
+            };
+            // The scores of the next tile for group g's rows, into S number buf.
+            auto scores = [&](int g, int buf) {
+                if (nt < 0) {
                     bar_wait(bQ, q_ph, ok);
                     q_ph ^= 1;
+                    nt = -nt;
                 }
-                --left;
                 bar_wait(bFull + 8 * kr.s, kr.ph, ok);
                 tc_after();
-                const uint32_t d = tmem + (n & 1) * kTile, ka = sKV + kr.s * slot_bytes;
+                const uint32_t d = tmem + buf * kTile, ka = sKV + kr.s * slot_bytes, qa = sQ + g * C::Q1;
+                const uint64_t dq = op_desc(qa, 16, 1024);
                 if constexpr (C::F8) {
                     // q's two parts one after the other
-                    const uint64_t dq = op_desc(sQ, 16, 1024);
                     const uint64_t dk = op_desc(ka, 16, 8 * a.pitch, a.pitch == 128 ? 2 : 4);
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
@@ -442,38 +454,69 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         mma_ss_f8(d, dq + (C::SUB >> 4) + 2 * k, dk + 2 * k, idS, 1);
                     }
                 } else {
-                    const uint64_t dq = op_desc(sQ, 16, 1024), dk = op_desc(ka, 16, 1024);
+                    const uint64_t dk = op_desc(ka, 16, 1024);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t st = (uint64_t)(((k >> 2) * C::SUB + (k & 3) * 32) >> 4);
                         mma_ss(d, dq + st, dk + st, idS, k > 0);
                     }
                 }
-                tc_commit(bEmpty + 8 * kr.s);
-                tc_commit(bS + 8 * (n & 1));
-                if (left == 0)
-                    tc_commit(bQFree);
-                kr.step(2, slots);
-                return true;
+                tc_commit(bS + 8 * buf);
+                if (!C::TWO || g == 1) {
+                    tc_commit(bEmpty + 8 * kr.s);
+                    if (--left == 0)
+                        tc_commit(bQFree);
+                    kr.step(2, slots);
+                }
             };
-            int i = 0, t = 0, nt_i = 0; // tile, its number in its segment, that one's tiles
-            bool more = scores(0);
-            nt_i = nt;
-            while (more) {
-                more = scores(i + 1);
+            // Tile i's product with the values into O number buf.
+            auto values = [&](int i, int buf, uint32_t p_ph, bool begun) {
                 const uint32_t vfull = C::F8 ? bVFull + 8 * (i & 1) : bFull + 8 * vr.s;
                 bar_wait(vfull, C::F8 ? (i >> 1) & 1 : vr.ph, ok);
-                bar_wait(bP + 8 * (i & 1), (i >> 1) & 1, ok);
+                bar_wait(bP + 8 * buf, p_ph, ok);
                 tc_after();
-                const uint32_t add = t >= 2 || *(volatile int *)&s_acc[i & 1];
+                const uint32_t add = begun || *(volatile int *)&s_acc[buf];
                 const uint32_t va = C::F8 ? sV + (i & 1) * C::SLOT : sKV + vr.s * slot_bytes;
                 const uint64_t dv = op_desc(va, C::SUB, 1024);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + kColO + (i & 1) * 128, tmem + (i & 1) * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
-                tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s);
-                tc_commit(bO + 8 * (i & 1));
-                vr.step(2, slots);
+                    mma_ts(tmem + kColO + buf * 128, tmem + buf * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
+                tc_commit(bO + 8 * buf);
+                if (!C::TWO || buf == 1) {
+                    tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s);
+                    vr.step(2, slots);
+                }
+            };
+            int i = 0, t = 0; // tile, its number in its segment
+            bool more = next();
+            if (more) {
+                scores(0, 0);
+                if constexpr (C::TWO)
+                    scores(1, 1);
+            }
+            int nt_i = nt; // its segment's tiles
+            while (more) {
+                more = next();
+                const bool crosses = more && nt < 0; // into the next segment
+                if constexpr (C::TWO) {
+                    values(i, 0, i & 1, t > 0);
+                    if (more && !crosses)
+                        scores(0, 0);
+                    values(i, 1, i & 1, t > 0);
+                    if (more) {
+                        if (crosses)
+                            scores(0, 0);
+                        scores(1, 1);
+                    }
+                } else {
+                    // one tile ahead, but not if the next segment's Q is waited for
+                    const bool ahead = more && (!crosses || bar_test(bQ, q_ph));
+                    if (ahead)
+                        scores(0, (i + 1) & 1);
+                    values(i, i & 1, (i >> 1) & 1, t >= 2);
+                    if (more && !ahead)
+                        scores(0, (i + 1) & 1);
+                }
                 ++i;
                 if (++t == nt_i) {
                     t = 0;
@@ -482,52 +525,62 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
             // every product is complete before the tensor memory is freed
             bool done = true;
-            if (i >= 2)
-                bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, done);
-            if (i >= 1)
-                bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, done);
+            if constexpr (C::TWO) {
+                for (int b = 0; b < 2 && i > 0; ++b)
+                    bar_wait(bO + 8 * b, (i - 1) & 1, done);
+            } else {
+                if (i >= 2)
+                    bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, done);
+                if (i >= 1)
+                    bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, done);
+            }
             ok = ok && done;
         }
         __syncwarp();
-    } else if (warp >= kAux) {
-        // ---- Q, the values next to the end, 8-bit values -> fp16 ---------------
-        constexpr int AT = 32 * C::AUX;
-        const int ct = tid - 32 * kAux;
-        Ring seg{0, 0}, vr{C::F8 ? 1 : 0, 0};
+    } else if (warp >= kQ && warp < C::kV) {
+        // ---- Q -----------------------------------------------------------
+        // The rows in the operand's layout, once per copy. With 8-bit keys each
+        // row is scaled by the power of two that brings its largest value into
+        // [2^7, 2^8) and split in two 8-bit parts, 4 bits each of its 8: exact
+        // for values down to 2^-2, below it off by at most 2^-10, i.e. 2^-17 of
+        // the largest. A negative scale's sign goes to q, so that the largest
+        // score is the largest exponent.
+        constexpr int QT = 32 * C::QW, CH = D / 8;           // 16-byte chunks of a row
+        constexpr int ALL = (C::TWO ? 256 : MT) * CH / QT, N = ALL < 16 ? ALL : 16;
+        const int ct = tid - 32 * kQ;
+        const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t inv_g = 0xffffffffu / (uint32_t)G + 1; // x / G = (x inv_g) >> 32 for x G < 2^32
+        Ring seg{0, 0};
         uint32_t free_ph = 1; // the operand is free at first
-        int i = 0, segs = 0;
+        int segs = 0;
         for (;;) {
             bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
             __syncwarp();
-            const Seg sg = s_seg[seg.s];
-            if (!led || sg.nt == 0)
+            if (!led || s_seg[seg.s].nt == 0)
                 break;
+            const int tok = s_seg[seg.s].tok, n = s_seg[seg.s].n, h = s_seg[seg.s].h, g0 = s_seg[seg.s].rt * MT;
             seg.step(1, kRing);
-            // Q, once per copy of the rows. With 8-bit keys each row is scaled by
-            // the power of two that brings its largest value into [2^7, 2^8) and
-            // split in two 8-bit parts, 4 bits each of its 8: exact for values
-            // down to 2^-2, below it off by at most 2^-10, i.e. 2^-17 of the
-            // largest. A negative scale's sign goes to q, so that the largest
-            // score is the largest exponent.
-            constexpr int CH = D / 8, ALL = MT * CH / AT, N = ALL < 8 ? ALL : 8;
-            const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+            const int t0 = g0 / G, rem0 = g0 - t0 * G;
 #pragma unroll 1
             for (int k0 = 0; k0 < ALL; k0 += N) {
                 uint4 v[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * AT, g = sg.rt * MT + idx / CH, ti = g / G;
+                    const int idx = ct + (k0 + k) * QT, x = rem0 + idx / CH;
+                    const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
                     v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ti < sg.n)
-                        v[k] = *reinterpret_cast<const uint4 *>(
-                            p.q + (sg.tok + ti) * p.ld_q + (long long)(sg.h * G + g - ti * G) * D + 8 * (idx % CH));
+                    if (ti < n)
+                        v[k] = *reinterpret_cast<const uint4 *>(p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D +
+                                                                8 * (idx % CH));
                 }
                 if (k0 == 0)
                     bar_wait(bQFree, free_ph, ok); // the last segment's scores are done
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * AT, qr = idx / CH, c = idx % CH;
+                    const int idx = ct + (k0 + k) * QT, qr = idx / CH, c = idx % CH;
+                    uint8_t *dst = smem + (C::TWO ? (qr >> 7) * C::Q1 : 0);
+                    const int r = C::TWO ? qr & 127 : qr;
                     const uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
                     if constexpr (C::F8) {
                         float f[8], mx = 0.0f;
@@ -560,12 +613,12 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         for (int cp = 0; cp < C::COPIES; ++cp)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<uint2 *>(smem + e * C::SUB + op_off(qr + cp * MT, c >> 1) + 8 * (c & 1)) =
+                                *reinterpret_cast<uint2 *>(dst + e * C::SUB + op_off(r + cp * MT, c >> 1) + 8 * (c & 1)) =
                                     make_uint2(part[e][0], part[e][1]);
                     } else {
 #pragma unroll
                         for (int cp = 0; cp < C::COPIES; ++cp)
-                            *reinterpret_cast<uint4 *>(smem + op_off(qr + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst + op_off(r + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
@@ -575,9 +628,23 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 bar_arrive(bQ);
-
-            for (int t = 0; t < sg.nt; ++t) {
-                const bool is_tail = t >= sg.first_tail;
+        }
+    } else if (warp >= C::kV) {
+        // ---- the values next to the end, 8-bit values -> fp16 -------------------
+        constexpr int VT = 32 * C::VW;
+        const int ct = tid - 32 * C::kV;
+        Ring seg{0, 0}, vr{C::F8 ? 1 : 0, 0};
+        int i = 0;
+        for (;;) {
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            __syncwarp();
+            const int nt = s_seg[seg.s].nt, first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
+            const int key0 = s_seg[seg.s].key0, end = s_seg[seg.s].end, len = s_seg[seg.s].len;
+            if (!led || nt == 0)
+                break;
+            seg.step(1, kRing);
+            for (int t = 0; t < nt; ++t) {
+                const bool is_tail = t >= first_tail;
                 uint8_t *vs; // the tile's values, 16 bits
                 if constexpr (C::F8) {
                     bar_wait(bFull + 8 * vr.s, vr.ph, ok);
@@ -585,18 +652,18 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     __syncwarp();
                     const uint8_t *src = smem + (sKV - sQ) + vr.s * slot_bytes;
                     vs = smem + (sV - sQ) + (i & 1) * C::SLOT;
-                    constexpr int M = kTile * D / 16 / AT;
+                    constexpr int M = kTile * D / 16 / VT;
                     uint4 v[M];
 #pragma unroll
                     for (int k = 0; k < M; ++k) {
-                        const int idx = ct + k * AT, row = idx / (D / 16), c = idx % (D / 16);
+                        const int idx = ct + k * VT, row = idx / (D / 16), c = idx % (D / 16);
                         // the copies' swizzle: of 128 bytes, or of 64 with rows of 64
                         const int x = c ^ (a.pitch == 128 ? row & 7 : (row >> 1) & 3);
                         v[k] = *reinterpret_cast<const uint4 *>(src + row * a.pitch + 16 * x);
                     }
 #pragma unroll
                     for (int k = 0; k < M; ++k) {
-                        const int idx = ct + k * AT, row = idx / (D / 16), c = idx % (D / 16);
+                        const int idx = ct + k * VT, row = idx / (D / 16), c = idx % (D / 16);
                         *reinterpret_cast<uint4 *>(vs + op_off(row, 2 * c)) =
                             make_uint4(e4m3x2_to_f16x2(v[k].x & 0xffffu), e4m3x2_to_f16x2(v[k].x >> 16),
                                        e4m3x2_to_f16x2(v[k].y & 0xffffu), e4m3x2_to_f16x2(v[k].y >> 16));
@@ -609,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         bar_arrive(bEmpty + 8 * vr.s);
                     vr.step(2, slots);
                     if (is_tail)
-                        named_sync<AT>(4); // the rows below are other warps' too
+                        named_sync<VT>(4); // the rows below are other warps' too
                 } else {
                     bar_wait(bFull + 8 * vr.s, vr.ph, ok); // the keys, passed on
                     __syncwarp();
@@ -620,19 +687,19 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     __syncwarp();
                     vs = smem + (sKV - sQ) + vr.s * slot_bytes;
                 }
+                const int tail = (tail_index + t - first_tail) % kRing;
                 if (is_tail) {
                     // A tail tile: values behind the end become zero, and of the
                     // drafted tokens' those that are not finite are marked.
-                    const int kt = sg.key0 + t * kTile;
-                    uint32_t *odd_keys = s_odd[(sg.tail_index + t - sg.first_tail) % kRing];
+                    const int kt = key0 + t * kTile;
 #pragma unroll 1
-                    for (int vrow = ct; vrow < kTile; vrow += AT) {
+                    for (int vrow = ct; vrow < kTile; vrow += VT) {
                         bool odd = false;
-                        if (kt + vrow >= sg.end) {
+                        if (kt + vrow >= end) {
 #pragma unroll
                             for (int c = 0; c < D / 8; ++c)
                                 *reinterpret_cast<uint4 *>(vs + op_off(vrow, c)) = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (kt + vrow >= sg.len) {
+                        } else if (kt + vrow >= len) {
                             constexpr uint32_t EXP = C::F8 ? 0x7c007c00u : 0x7f807f80u;
 #pragma unroll
                             for (int c = 0; c < D / 8; ++c) {
@@ -644,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         __syncwarp();
                         const uint32_t ob = __ballot_sync(~0u, odd);
                         if (lane == 0)
-                            odd_keys[vrow >> 5] = ob;
+                            s_odd[tail][vrow >> 5] = ob;
                     }
                 }
                 if (C::F8 || is_tail)
@@ -653,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 if (lane == 0) {
                     bar_arrive(C::F8 ? bVFull + 8 * (i & 1) : bEmpty + 8 * vr.s);
                     if (is_tail)
-                        bar_arrive(bTail + 8 * ((sg.tail_index + t - sg.first_tail) % kRing));
+                        bar_arrive(bTail + 8 * tail);
                 }
                 if (!C::F8)
                     vr.step(1, slots);
@@ -663,10 +730,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     } else {
         // ---- the softmax -------------------------------------------------
         const int grp = warp >> 2, wq = warp & 3;
-        const int quad = wq / (MT / 32), row = (wq % (MT / 32)) * 32 + lane; // copy, row of the tile
+        const int quad = wq / (C::ROWS / 32), row = (wq % (C::ROWS / 32)) * 32 + lane; // copy, row of the group's
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t tS = tmem + grp * kTile + lanes, tO = tmem + kColO + grp * 128 + lanes;
         const int gtid = tid & (kGroup - 1);
+        const float base_factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
         Ring seg{0, 0};
         uint32_t s_ph = 0; // of this group's next tile: S, P, O take the same turns
         int i0 = 0, segs = 0;
@@ -676,8 +744,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             const Seg sg = s_seg[seg.s];
             if (!led || sg.nt == 0)
                 break;
-            const bool both = sg.nt > 1, takes = both || (i0 & 1) == grp;
-            const int g = sg.rt * MT + row, ti = g / G;
+            const bool both = !C::TWO && sg.nt > 1; // groups that have tiles of it
+            const bool takes = C::TWO || both || (i0 & 1) == grp;
+            const int t0 = C::TWO ? 0 : (grp ^ i0) & 1, dt = C::TWO ? 1 : 2;
+            const int trow = C::TWO ? grp * 128 + row : row; // row of the tile
+            const int g = sg.rt * MT + trow, ti = g / G;
             const bool live = ti < sg.n;
             const int tok_i = live ? ti : 0;
             const bool warp_live = __any_sync(~0u, live);
@@ -686,12 +757,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             rq.n = sg.n;
             rq.len = sg.len;
             const uint64_t first = takes && sg.first_tail < sg.nt ? tree_bits(p, rq, tok_i) : 0;
-            const float base_factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
             float factor = fmaxf(base_factor, 1e-37f); // a scale of zero: all scores alike
             float m = -INFINITY, l = 0.0f;             // reference (base 2), sum
-            const int t0 = (grp ^ i0) & 1;
 
-            for (int t = t0; t < sg.nt; t += 2) {
+#pragma unroll 1
+            for (int t = t0; t < sg.nt; t += dt) {
                 const int kt = sg.key0 + t * kTile;
                 bar_wait(bS + 8 * grp, s_ph, ok);
                 __syncwarp();
@@ -700,36 +770,32 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     s_acc[grp] = 0;
                 if constexpr (C::F8)
                     if (t == t0)
-                        factor = fmaxf(base_factor * s_f[segs & 3][row], 1e-37f);
+                        factor = fmaxf(base_factor * s_f[segs & 3][trow], 1e-37f);
                 // Tiles that reach the drafted tokens or the end, or hold a key
                 // without a page.
                 const uint32_t *bad = s_bad[(i0 + t) % kTiles];
                 const bool is_tail = t >= sg.first_tail;
                 const bool masked = is_tail || (bad[0] | bad[1] | bad[2] | bad[3]);
-                uint32_t vis[C::NCH];
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < C::NCH; c += 2) {
-                        const int ch = quad * C::NCH + c;
-                        const uint64_t v = visible(p, rq, tok_i, first, kt + 32 * ch, sg.end);
-                        vis[c] = (uint32_t)v & ~bad[ch];
-                        if (C::NCH > 1)
-                            vis[c + (C::NCH > 1)] = (uint32_t)(v >> 32) & ~bad[ch + 1];
-                    }
-                }
+                // the keys of this copy's chunk c that the row sees
+                auto seen = [&](int c) {
+                    const int ch = quad * C::NCH + c;
+                    return (uint32_t)visible(p, rq, tok_i, first, kt + 32 * ch, sg.end) & ~bad[ch];
+                };
                 if (warp_live) {
                     uint32_t s[32];
-                    auto chunk = [&](int c) { // of this copy's: scores, unseen keys' at -infinity
+                    auto chunk = [&](int c) { // its scores, unseen keys' at -infinity
                         tmem_ld32(tS + 32 * (quad * C::NCH + c), s);
                         tmem_ld_wait(s);
-                        if (masked)
+                        if (masked) {
+                            const uint32_t vis = seen(c);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!((vis[c] >> e) & 1))
+                                if (!((vis >> e) & 1))
                                     s[e] = 0xff800000u;
+                        }
                     };
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < C::NCH; ++c) {
                         chunk(c);
 #pragma unroll
@@ -743,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         const float corr = grow ? exp2_fast(m - top) : 1.0f;
                         m = grow ? top : m;
                         l *= corr;
-                        if (t >= 2) { // this group's last product is done: S was issued after it
+                        if (t >= dt) { // this group's last product is done: S was issued after it
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t o[16];
@@ -760,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
                     // small ones, 2^-25); their sum l is of the unrounded ones.
                     float2 sum[2] = {};
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < C::NCH; ++c) {
                         if (C::NCH > 1)
                             chunk(c);
@@ -796,7 +862,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         // the rows that do, and taken out of the slot.
                         uint8_t *vs;
                         if constexpr (C::F8)
-                            vs = smem + (sV - sQ) + grp * C::SLOT;
+                            vs = smem + (sV - sQ) + ((i0 + t) & 1) * C::SLOT;
                         else
                             vs = smem + (sKV - sQ) + (2 * (i0 + t) + 1) % slots * slot_bytes;
                         __syncwarp();
@@ -804,18 +870,14 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
-                            if (t < 2)
+                            if (t < dt)
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = 0u;
 #pragma unroll 1
                             for (int k = 0; k < 32 * C::NCH; ++k) {
                                 const int kr = quad * 32 * C::NCH + k; // row of the slot
-                                uint32_t v = vis[0];
-#pragma unroll
-                                for (int x = 1; x < C::NCH; ++x)
-                                    v = k >> 5 == x ? vis[x] : v;
-                                if (!((odd[kr >> 5] >> (kr & 31)) & 1) || !((v >> (k & 31)) & 1))
+                                if (!((odd[kr >> 5] >> (kr & 31)) & 1) || !((seen(k >> 5) >> (k & 31)) & 1))
                                     continue;
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
@@ -829,7 +891,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                             tmem_st16(tO + c, o);
                         }
                         tmem_st_wait();
-                        named_sync<kGroup>(2 + grp);
+                        // every group that reads the slot has read it
+                        if constexpr (C::TWO)
+                            named_sync<2 * kGroup>(1);
+                        else
+                            named_sync<kGroup>(2 + grp);
                         if ((odd[wq] >> lane) & 1) {
                             constexpr uint16_t EXP = C::F8 ? 0x7c00 : 0x7f80;
                             for (int e = 0; e < D; ++e) {
@@ -839,9 +905,12 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                             }
                         }
                         if (gtid == 0)
-                            s_acc[grp] = t < 2;
+                            s_acc[grp] = t < dt;
                         fence_async_smem();
-                        named_sync<kGroup>(2 + grp);
+                        if constexpr (C::TWO)
+                            named_sync<2 * kGroup>(1);
+                        else
+                            named_sync<kGroup>(2 + grp);
                     }
                 }
                 tc_before();
@@ -852,128 +921,79 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
 
             // ---- the segment's end -----------------------------------------------
+            // The sources of a row (its copies, in one group or both) are joined 16
+            // columns at a time through shared memory, and written by four threads
+            // a row, so that the stores are whole sectors.
             if (takes) {
                 bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
                 __syncwarp();
                 tc_after();
-                const long long tk = sg.tok + tok_i;
-                const int hq = sg.h * G + g - ti * G;
-                float *part = part_of(p, blockIdx.x, sg.which, MT, D);
-                uint16_t *orow = p.out + tk * p.ld_out + (long long)hq * D;
-                float *prow = part + (size_t)row * D;
-                auto put_sums = [&](float top, float sum) {
-                    if (!sg.whole) {
-                        part[MT * D + row] = top;
-                        part[MT * D + MT + row] = sum;
-                    } else if (p.lse) {
+                const int nsrc = both ? 2 * C::COPIES : C::COPIES;
+                const int base = both ? 0 : grp * C::COPIES, src = grp * C::COPIES + quad; // first source, this one
+                float4 *buf = reinterpret_cast<float4 *>(smem + (sJoin - sQ));
+                float *part = part_of(p, blockIdx.x, sg.which, MT, D) + (C::TWO ? grp * 128 * D : 0);
+                auto sync = [&] {
+                    if (both)
+                        named_sync<2 * kGroup>(1);
+                    else
+                        named_sync<kGroup>(2 + grp);
+                };
+                s_m[src][row] = m;
+                s_l[src][row] = l;
+                sync();
+                float top = -INFINITY, sum = 0.0f;
+                for (int c = base; c < base + nsrc; ++c)
+                    top = fmaxf(top, s_m[c][row]);
+                for (int c = base; c < base + nsrc; ++c) { // one that saw nothing has l = 0 (or NaN)
+                    const float mc = s_m[c][row], lc = s_l[c][row];
+                    sum += mc == -INFINITY ? lc : lc * exp2_fast(mc - top);
+                }
+                float f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
+                if (sg.whole) // the sums' inverse and the values' scale, on the way
+                    f *= sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
+                if (src == base) {
+                    const long long tk = sg.tok + tok_i;
+                    const int hq = sg.h * G + g - ti * G;
+                    s_row[grp][row] = live ? tk * p.ld_out + (long long)hq * D : -1;
+                    if (live && !sg.whole) {
+                        part[(C::TWO ? (256 - grp * 128) * D + grp * 128 : MT * D) + row] = top;
+                        part[(C::TWO ? (256 - grp * 128) * D + 256 + grp * 128 : MT * D + MT) + row] = sum;
+                    } else if (live && p.lse) {
                         p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
-                };
-                // Joins the NSRC sources of a row, 16 columns at a time through
-                // shared memory, each thread writing CW columns of its row.
-                auto finish = [&](auto nsrc) {
-                    constexpr int NSRC = decltype(nsrc)::value, CW = 16 / NSRC;
-                    constexpr bool BOTH = NSRC == 2 * C::COPIES;
-                    const int src = BOTH ? grp * C::COPIES + quad : quad;
-                    auto sync = [&] {
-                        if constexpr (BOTH)
-                            named_sync<2 * kGroup>(1);
-                        else
-                            named_sync<kGroup>(2 + grp);
-                    };
-                    const int base = BOTH ? 0 : grp * C::COPIES; // first source's entries
-                    float4 *buf = reinterpret_cast<float4 *>(smem + (sJoin - sQ)) + base * MT * 4;
-                    s_m[base + src][row] = m;
-                    s_l[base + src][row] = l;
-                    sync();
-                    float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < NSRC; ++c)
-                        top = fmaxf(top, s_m[base + c][row]);
-#pragma unroll
-                    for (int c = 0; c < NSRC; ++c) { // one that saw nothing has l = 0 (or NaN)
-                        const float mc = s_m[base + c][row], lc = s_l[base + c][row];
-                        sum += mc == -INFINITY ? lc : lc * exp2_fast(mc - top);
-                    }
-                    const float f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
-                    const float inv = sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
-                    if (live && src == 0)
-                        put_sums(top, sum);
-                    const int sw = (row >> 1) & 3;
+                }
+                const int sw = (row >> 1) & 3, wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
+                const long long *rows = s_row[both ? 0 : grp];
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        if (warp_live) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + c0, o);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                buf[(src * MT + row) * 4 + (e ^ sw)] =
-                                    make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                                __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
-                        }
-                        sync();
-                        if (live) {
-                            float x[CW] = {};
-                            const int col = src * CW;
-#pragma unroll
-                            for (int c = 0; c < NSRC; ++c) {
-                                const float *b = reinterpret_cast<const float *>(buf + (c * MT + row) * 4);
-                                if constexpr (CW == 2) {
-                                    const float2 y = *reinterpret_cast<const float2 *>(b + (((col >> 2) ^ sw) << 2) + (col & 3));
-                                    x[0] += y.x;
-                                    x[1] += y.y;
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < CW; e += 4) {
-                                        const float4 y = *reinterpret_cast<const float4 *>(b + ((((col + e) >> 2) ^ sw) << 2));
-                                        x[e] += y.x;
-                                        x[e + 1] += y.y;
-                                        x[e + 2] += y.z;
-                                        x[e + 3] += y.w;
-                                    }
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < CW; e += 2) {
-                                if (sg.whole)
-                                    *reinterpret_cast<uint32_t *>(orow + c0 + col + e) = pack2<false>(x[e] * inv, x[e + 1] * inv);
-                                else
-                                    *reinterpret_cast<float2 *>(prow + c0 + col + e) = make_float2(x[e], x[e + 1]);
-                            }
-                        }
-                        sync();
-                    }
-                };
-                if (both) {
-                    finish(std::integral_constant<int, 2 * C::COPIES>{});
-                } else if constexpr (C::COPIES > 1) {
-                    finish(std::integral_constant<int, C::COPIES>{});
-                } else {
-                    const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
-                    if (live)
-                        put_sums(m, l);
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                    if (warp_live) {
                         uint32_t o[16];
-                        tmem_ld16(tO + c, o);
-                        if (live && sg.whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(orow + c);
+                        tmem_ld16(tO + c0, o);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint32_t b[4];
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    b[x] = pack2<false>(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-                                dst[e] = make_uint4(b[0], b[1], b[2], b[3]);
-                            }
-                        } else if (live) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(prow + c);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        }
-                        __syncwarp();
+                        for (int e = 0; e < 4; ++e)
+                            buf[(src * C::ROWS + row) * 4 + (e ^ sw)] =
+                                make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                            __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
                     }
+                    sync();
+#pragma unroll 1
+                    for (int w = wtid; w < C::ROWS * 4; w += wth) {
+                        const int rr = w >> 2, e = w & 3;
+                        const long long off = rows[rr];
+                        if (off < 0)
+                            continue;
+                        const float4 *b = buf + (base * C::ROWS + rr) * 4 + (e ^ ((rr >> 1) & 3));
+                        float4 x = b[0];
+                        for (int c = 1; c < nsrc; ++c) {
+                            const float4 y = b[c * C::ROWS * 4];
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        if (sg.whole)
+                            *reinterpret_cast<uint2 *>(p.out + off + c0 + 4 * e) = make_uint2(pack2<false>(x.x, x.y), pack2<false>(x.z, x.w));
+                        else
+                            *reinterpret_cast<float4 *>(part + (size_t)rr * D + c0 + 4 * e) = x;
+                    }
+                    sync();
                 }
                 tc_before();
             }
@@ -1151,26 +1171,31 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
     return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);
 }
 
+// Rows of a tile: what a request has on average, at least 32.
+int row_tile(int T, int R, int Hq, int Hkv)
+{
+    const long long rows = (long long)((T + R - 1) / R) * (Hq / Hkv);
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
+
 template <int D, int KV>
 cudaError_t launch_d(const AttnProblem &p, int num_sms, cudaStream_t stream)
 {
     const int grid = std::min(num_sms, kMaxGrid);
-    const int G = p.Hq / p.cache.heads;
-    const long long rows = (long long)((p.T + p.R - 1) / p.R) * G;
-    return rows <= 32   ? launch_t<D, KV, 32>(p, grid, stream)
-           : rows <= 64 ? launch_t<D, KV, 64>(p, grid, stream)
-                        : launch_t<D, KV, 128>(p, grid, stream);
+    switch (row_tile(p.T, p.R, p.Hq, p.cache.heads)) {
+    case 32: return launch_t<D, KV, 32>(p, grid, stream);
+    case 64: return launch_t<D, KV, 64>(p, grid, stream);
+    case 128: return launch_t<D, KV, 128>(p, grid, stream);
+    default: return launch_t<D, KV, 256>(p, grid, stream);
+    }
 }
 
 } // namespace
 
 size_t attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D)
 {
-    (void)T;
-    (void)R;
-    (void)Hq;
-    (void)Hkv;
-    return 2 * kMaxGrid * sizeof(Split) + (size_t)2 * kMaxGrid * kMaxMT * (D + 2) * sizeof(float);
+    return 2 * kMaxGrid * sizeof(Split) +
+           (size_t)2 * kMaxGrid * row_tile(T, R, Hq, Hkv) * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnProblem &p, int num_sms, cudaStream_t stream)

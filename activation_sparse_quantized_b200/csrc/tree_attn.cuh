@@ -12,7 +12,6 @@ namespace {
 constexpr int kBN = 64;        // keys per unit
 constexpr int kItemCost = 2;   // what an item costs beside its units, in units
 constexpr int kMaxGrid = 160;  // one CTA per SM
-constexpr int kMaxMT = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
