@@ -19,10 +19,10 @@
 // directly.
 //
 // Both products are tcgen05.mma of 128 rows and 128 keys. The warps:
-//  * one walks the run, looks up the pages and copies keys and values by the
-//    box (cp.async.bulk.tensor, swizzled), two ring slots per 128 keys; what
-//    lies behind a segment's keys, and bad pages, is filled with zeros by a
-//    box outside the map;
+//  * one walks the run and copies keys, one copies values, by the box of a
+//    page's rows (cp.async.bulk.tensor, swizzled) into a ring, two slots per
+//    128 keys; what lies behind a segment's keys, and bad pages, is filled with
+//    zeros by a box outside the map;
 //  * one thread issues S = Q K^T (both from shared memory) into one of two
 //    accumulators, one tile ahead and across segments, and O += P V with P
 //    read from tensor memory, where it takes S's place;
@@ -60,18 +60,18 @@ namespace {
 
 constexpr int kTile = 128; // keys per product
 constexpr int kGroup = 128; // threads of a softmax group
-constexpr int kSoftWarps = 8, kProducer = 8, kIssuer = 9, kQ = 10; // warps
+constexpr int kSoftWarps = 8, kKeys = 8, kValues = 9, kIssuer = 10, kQ = 11; // warps
 constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
 constexpr int kTiles = 16;      // tiles that are
-constexpr unsigned long long kSegWaitNs = 2000000000ull;
+constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 2000000ull;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_;
     static constexpr bool F8 = KV == SGQ_TYPE_E4M3, TWO = MT == 256;
-    static constexpr int QW = F8 ? 2 : 1, VW = F8 ? 4 : 1;    // warps for Q, for the values
+    static constexpr int QW = F8 && !TWO ? 1 : 2, VW = !F8 ? 1 : TWO ? 2 : 4; // warps for Q, for the values read
     static constexpr int kV = kQ + QW, THREADS = 32 * (kV + VW);
     static constexpr int ROWS = TWO ? 128 : MT;               // of a group
     static constexpr int COPIES = 128 / ROWS, NCH = 4 / COPIES; // copies of the rows, 32-key chunks of each
@@ -100,7 +100,7 @@ struct TcArgs {
 
 // What a CTA's warps need of a segment (nt = 0: the run has ended).
 struct Seg {
-    int nt;                     // tiles
+    int nt, r;                  // tiles, request
     int tok, n, len;            // the request's first row, new tokens, cached ones
     int key0, end;              // its keys
     int h, rt;                  // key head, row tile
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ Request s_rq;
     __shared__ Seg s_seg[kRing];
     __shared__ float s_m[2 * C::COPIES][C::ROWS], s_l[2 * C::COPIES][C::ROWS];
-    __shared__ long long s_row[2][C::ROWS]; // where a row's output goes, -1: nowhere
+    __shared__ long long s_row[2][C::ROWS]; // where a row's output goes
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
     __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
     __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    } else if (warp == kProducer && lane == 0) {
+    } else if (warp == kKeys && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int s = 0; s < C::MAX_SLOTS; ++s) {
@@ -266,15 +266,16 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     }
     __syncthreads();
 
-    if (warp == kProducer) {
+    if (warp == kKeys || warp == kValues) {
         // ---- the run's segments; pages -> slots ------------------------------
-        // Lane x of round j copies piece x + 32 j of a slot: a box of `box` rows
-        // and 128 bytes (one round for pages of at least 8 slots). The pages of
-        // the next two tiles are looked up ahead.
+        // Lane x knows piece x of a slot: a box of `box` rows and 128 bytes (all
+        // pieces, for pages of at least 8 slots; the others are looked up when
+        // their turn comes). The pages of the next two tiles are looked up ahead.
+        const bool keys = warp == kKeys;
         Walk walk;
-        walk.u = u;
-        walk.u_end = u_end;
-        if (u < u_end) {
+        if (keys && u < u_end) {
+            walk.u = u;
+            walk.u_end = u_end;
             walk.r = s_r;
             walk.base = s_first;
             walk.rq = s_rq;
@@ -282,8 +283,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const uint32_t bytes = C::F8 ? kTile * D : C::SLOT; // of one slot's boxes
         constexpr int PARTS = C::F8 ? 1 : C::NSUB;          // boxes side by side in a row
         const int row_bytes = C::F8 ? a.pitch : 128;
-        const int pieces = kTile / a.box * PARTS, rounds = (pieces + 31) / 32;
+        const int pieces = kTile / a.box * PARTS, near = min(pieces, 32);
         const int page = p.cache.page, page_up = kTile / page, slot_up = kTile % page;
+        const CUtensorMap *map = keys ? &kmap : &vmap;
         auto step = [&](int &g, int &s) { // one tile on
             g += page_up;
             s += slot_up;
@@ -292,38 +294,53 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 ++g;
             }
         };
-        Ring ring{0, 0}, seg{0, 0};
-        Split split[2] = {};
-        int i = 0, tails = 0, issued = 0; // tiles, tail tiles, slots so far
+        Ring ring{keys ? 0 : 1, 0}, seg{0, 0};
+        Split split0{}, split1{};
+        int i = 0, tails = 0; // tiles, tail tiles so far
         for (;;) {
-            const bool more = __all_sync(~0u, ok) && walk.next(p, G, MT);
-            const int nt = more ? (walk.nu + 1) / 2 : 0;
-            const int key0 = walk.j0 * kBN, end = walk.key_end();
-            const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
-            bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSegWaitNs);
-            __syncwarp();
-            if (lane == 0) {
-                Seg &sg = s_seg[seg.s];
-                sg.nt = nt;
-                sg.tok = walk.rq.tok;
-                sg.n = walk.rq.n;
-                sg.len = walk.rq.len;
-                sg.key0 = key0;
-                sg.end = end;
-                sg.h = walk.h;
-                sg.rt = walk.rt;
-                sg.first_tail = first_tail;
-                sg.tail_index = tails;
-                sg.whole = walk.whole();
-                sg.which = walk.j0 == 0;
-                bar_arrive(bSeg + 8 * seg.s);
+            int nt, r, key0, end, h;
+            if (keys) {
+                const bool more = __all_sync(~0u, ok) && walk.next(p, G, MT);
+                nt = more ? (walk.nu + 1) / 2 : 0;
+                r = walk.r;
+                key0 = walk.j0 * kBN;
+                end = walk.key_end();
+                h = walk.h;
+                const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
+                bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSegWaitNs);
+                __syncwarp();
+                if (lane == 0) {
+                    Seg &sg = s_seg[seg.s];
+                    sg.nt = nt;
+                    sg.r = r;
+                    sg.tok = walk.rq.tok;
+                    sg.n = walk.rq.n;
+                    sg.len = walk.rq.len;
+                    sg.key0 = key0;
+                    sg.end = end;
+                    sg.h = h;
+                    sg.rt = walk.rt;
+                    sg.first_tail = first_tail;
+                    sg.tail_index = tails;
+                    sg.whole = walk.whole();
+                    sg.which = walk.j0 == 0;
+                    bar_arrive(bSeg + 8 * seg.s);
+                }
+                tails += max(0, nt - first_tail);
+            } else {
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+                __syncwarp();
+                nt = led ? s_seg[seg.s].nt : 0;
+                r = s_seg[seg.s].r;
+                key0 = s_seg[seg.s].key0;
+                end = s_seg[seg.s].end;
+                h = s_seg[seg.s].h;
             }
             seg.step(1, kRing);
-            if (!more)
+            if (nt == 0)
                 break;
-            tails += max(0, nt - first_tail);
-            const int32_t *table = p.table + (long long)walk.r * p.table_ld;
-            // this lane's box of round 0: page index, slot in it, ids of the next tiles
+            const int32_t *table = p.table + (long long)r * p.table_ld;
+            // this lane's box: page index, slot in it, ids of the next tiles
             const int first = key0 + lane / PARTS * a.box;
             int pg = first / page, sl = first - pg * page;
             auto look = [&](int t, int at_page) {
@@ -333,74 +350,80 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             int id0 = look(0, pg);
             step(pg_next, sl_next);
             int id1 = look(1, pg_next);
-            if (!walk.whole()) { // a part for join_kernel
-                Split &sp = split[walk.j0 == 0];
+            if (keys && !walk.whole()) { // a part for join_kernel
+                Split sp;
                 sp.c0 = cta_of(U, walk.item0, ctas);
                 sp.parts = cta_of(U, walk.item0 + walk.rq.tiles - 1, ctas) - sp.c0 + 1;
                 sp.tok = walk.rq.tok;
                 sp.n = walk.rq.n;
-                sp.h = walk.h;
+                sp.h = h;
                 sp.rt = walk.rt;
+                if (walk.j0 == 0)
+                    split1 = sp;
+                else
+                    split0 = sp;
             }
+#pragma unroll 1
             for (int t = 0; t < nt; ++t, ++i) {
                 int pg2 = pg_next, sl2 = sl_next;
                 step(pg2, sl2);
                 const int id2 = look(t + 2, pg2);
-                uint32_t *bad = s_bad[i % kTiles];
-                if (lane < 4)
-                    bad[lane] = 0;
-                // round 0's box; its page is waited for here
+                // this lane's box; its page is waited for here
                 const bool want = lane < pieces && first + t * kTile < end;
                 const bool good = want && id0 >= 0 && id0 < p.cache.num_pages;
                 const int pid = good ? id0 : p.cache.num_pages; // outside the map: zeros
                 const int slot = good ? sl : 0;
-                bool any = __any_sync(~0u, want && !good);
-                __syncwarp();
-                if (want && !good && lane % PARTS == 0)
-                    for (int k = 0; k < a.box; ++k) {
-                        const int b = lane / PARTS * a.box + k;
-                        atomicOr(&bad[b >> 5], 1u << (b & 31));
-                    }
-                for (int j = 1; j < rounds; ++j) { // boxes of fewer than 8 rows
-                    const int b = (lane + 32 * j) / PARTS, kb = key0 + t * kTile + b * a.box;
-                    if (kb < end) {
-                        const int id = table[kb / page];
-                        if (id < 0 || id >= p.cache.num_pages) {
-                            any = true;
-                            for (int k = 0; k < a.box; ++k)
-                                atomicOr(&bad[(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
+                if (keys) { // the keys without a page
+                    uint32_t *bad = s_bad[i % kTiles];
+                    if (lane < 4)
+                        bad[lane] = 0;
+                    bool any = __any_sync(~0u, want && !good);
+                    __syncwarp();
+                    if (any && want && !good && lane % PARTS == 0)
+                        for (int k = 0; k < a.box; ++k) {
+                            const int b = lane / PARTS * a.box + k;
+                            atomicOr(&bad[b >> 5], 1u << (b & 31));
+                        }
+                    for (int j = 32 + lane; j < pieces; j += 32) {
+                        const int b = j / PARTS, kb = key0 + t * kTile + b * a.box;
+                        if (kb < end) {
+                            const int id = table[kb / page];
+                            if (id < 0 || id >= p.cache.num_pages) {
+                                any = true;
+                                for (int k = 0; k < a.box; ++k)
+                                    atomicOr(&bad[(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
+                            }
                         }
                     }
-                }
-                if (any)
-                    set_status(p.status, SGQ_STATUS_BAD_INDEX);
-                __syncwarp();
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
-                    if (!__all_sync(~0u, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    ++issued;
-                    const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
-                    if (lane == 0)
-                        bar_expect(full, bytes);
+                    if (any)
+                        set_status(p.status, SGQ_STATUS_BAD_INDEX);
                     __syncwarp();
-                    const CUtensorMap *map = kv ? &vmap : &kmap;
-                    if (lane < pieces)
-                        tma_load_4d(dst + (lane % PARTS) * C::SUB + lane / PARTS * a.box * row_bytes, map, lane % PARTS * 64, slot,
-                                    walk.h, pid, full);
-                    for (int j = 1; j < rounds; ++j) {
-                        const int x = lane + 32 * j, b = x / PARTS, kb = key0 + t * kTile + b * a.box;
-                        int id = kb < end ? table[kb / page] : -1;
-                        if (id < 0 || id >= p.cache.num_pages)
-                            id = p.cache.num_pages;
-                        tma_load_4d(dst + (x % PARTS) * C::SUB + b * a.box * row_bytes, map, x % PARTS * 64, kb % page, walk.h, id,
-                                    full);
-                    }
-                    ring.step(1, slots);
                 }
+                bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    continue;
+                }
+                const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
+                if (lane == 0)
+                    bar_expect(full, bytes);
+                __syncwarp();
+                // one lane issues all of them: the copy takes its operands from
+                // registers that a warp shares
+#pragma unroll 4
+                for (int x = 0; x < near; ++x) {
+                    const int id = __shfl_sync(~0u, pid, x), s = __shfl_sync(~0u, slot, x);
+                    if (lane == 0)
+                        tma_load_4d(dst + (x % PARTS) * C::SUB + x / PARTS * a.box * row_bytes, map, x % PARTS * 64, s, h, id, full);
+                }
+                for (int x = 32 + lane; x < pieces; x += 32) {
+                    const int b = x / PARTS, kb = key0 + t * kTile + b * a.box;
+                    int id = kb < end ? table[kb / page] : -1;
+                    if (id < 0 || id >= p.cache.num_pages)
+                        id = p.cache.num_pages;
+                    tma_load_4d(dst + (x % PARTS) * C::SUB + b * a.box * row_bytes, map, x % PARTS * 64, kb % page, h, id, full);
+                }
+                ring.step(2, slots);
                 sl = sl_next;
                 pg_next = pg2;
                 sl_next = sl2;
@@ -408,13 +431,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 id1 = id2;
             }
         }
-        if (lane < 2)
-            static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split[1] : split[0];
-        // every copy has landed before the CTA ends, whatever went wrong
-        bool landed = true;
-        for (int n = max(0, issued - slots); n < issued; ++n)
-            bar_wait(bFull + 8 * (n % slots), (n / slots) & 1, landed);
-        ok = ok && landed;
+        if (keys && lane < 2)
+            static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split1 : split0;
     } else if (warp == kIssuer) {
         // ---- the products ------------------------------------------------
         if (lane == 0) {
@@ -921,9 +939,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
 
             // ---- the segment's end -----------------------------------------------
-            // The sources of a row (its copies, in one group or both) are joined 16
-            // columns at a time through shared memory, and written by four threads
-            // a row, so that the stores are whole sectors.
+            // The sources of a row (its copies, in one group or both) are joined
+            // through shared memory, as many columns at a time as the rows in use
+            // leave room for, and written by consecutive threads, so that the
+            // stores are whole sectors.
             if (takes) {
                 bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
                 __syncwarp();
@@ -954,7 +973,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 if (src == base) {
                     const long long tk = sg.tok + tok_i;
                     const int hq = sg.h * G + g - ti * G;
-                    s_row[grp][row] = live ? tk * p.ld_out + (long long)hq * D : -1;
+                    s_row[grp][row] = tk * p.ld_out + (long long)hq * D;
                     if (live && !sg.whole) {
                         part[(C::TWO ? (256 - grp * 128) * D + grp * 128 : MT * D) + row] = top;
                         part[(C::TWO ? (256 - grp * 128) * D + 256 + grp * 128 : MT * D + MT) + row] = sum;
@@ -962,34 +981,45 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
                 }
-                const int sw = (row >> 1) & 3, wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
+                const int wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
                 const long long *rows = s_row[both ? 0 : grp];
+                // live rows come first
+                const int used = min(C::ROWS, sg.n * G - sg.rt * MT - (C::TWO ? grp * 128 : 0));
+                int lg = 2; // 2^lg float4 a row and pass
+                while (lg < (D == 128 ? 5 : 4) && used * (C::COPIES << (lg + 1)) * 16 <= C::JOIN / 2)
+                    ++lg;
+                const int per_row = 1 << lg, mask = min(per_row, 8) - 1;
+                buf += base * (C::JOIN / 2 / 16 / C::COPIES);
+                const int stride = used << lg; // float4 of a source
+                auto place = [&](int rr, int e) { return (rr << lg) + (e ^ ((lg == 2 ? rr >> 1 : rr) & mask)); };
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 16) {
-                    if (warp_live) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + c0, o);
+                for (int c0 = 0; c0 < D; c0 += 4 * per_row) {
+                    if (warp_live)
+#pragma unroll 1
+                        for (int c = 0; c < per_row; c += 4) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c0 + 4 * c, o);
+                            if (live)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            buf[(src * C::ROWS + row) * 4 + (e ^ sw)] =
-                                make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                            __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
-                    }
+                                for (int e = 0; e < 4; ++e)
+                                    buf[(src - base) * stride + place(row, c + e)] =
+                                        make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                    __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                            __syncwarp();
+                        }
                     sync();
 #pragma unroll 1
-                    for (int w = wtid; w < C::ROWS * 4; w += wth) {
-                        const int rr = w >> 2, e = w & 3;
-                        const long long off = rows[rr];
-                        if (off < 0)
-                            continue;
-                        const float4 *b = buf + (base * C::ROWS + rr) * 4 + (e ^ ((rr >> 1) & 3));
+                    for (int w = wtid; w < used << lg; w += wth) {
+                        const int rr = w >> lg, e = w & (per_row - 1);
+                        const float4 *b = buf + place(rr, e);
                         float4 x = b[0];
+#pragma unroll 4
                         for (int c = 1; c < nsrc; ++c) {
-                            const float4 y = b[c * C::ROWS * 4];
+                            const float4 y = b[c * stride];
                             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                         }
                         if (sg.whole)
-                            *reinterpret_cast<uint2 *>(p.out + off + c0 + 4 * e) = make_uint2(pack2<false>(x.x, x.y), pack2<false>(x.z, x.w));
+                            *reinterpret_cast<uint2 *>(p.out + rows[rr] + c0 + 4 * e) = make_uint2(pack2<false>(x.x, x.y), pack2<false>(x.z, x.w));
                         else
                             *reinterpret_cast<float4 *>(part + (size_t)rr * D + c0 + 4 * e) = x;
                     }
@@ -1005,10 +1035,18 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             ++segs;
         }
     }
-    if (!ok || !led)
-        set_status(p.status, SGQ_STATUS_TIMEOUT);
     tc_before();
-    __syncthreads();
+    if (__syncthreads_or(!ok || !led)) {
+        // a wait ran out: copies that nothing waited for may be on their way
+        // still, and take microseconds
+        set_status(p.status, SGQ_STATUS_TIMEOUT);
+        unsigned long long t0, t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        do
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        while (t - t0 < kDrainNs);
+        __syncthreads();
+    }
     if (warp == kIssuer)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
