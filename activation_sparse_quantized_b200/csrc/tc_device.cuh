@@ -1,10 +1,8 @@
-// tc_device.cuh -- barriers, bulk tensor copies and tensor-core instructions
-// (mbarrier, cp.async.bulk.tensor, tcgen05) of the attention kernels.
+// tc_device.cuh -- barriers, copies and tensor-core instructions (mbarrier,
+// cp.async, tcgen05) of the attention kernel.
 #pragma once
 
 #include "sgq_device.cuh"
-
-#include <cuda.h>
 
 namespace sgq {
 
@@ -23,11 +21,18 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// This thread's arrival, and `bytes` more to come from bulk copies.
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+// 16 bytes into shared memory, or zeros.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool take)
 {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(take ? 16 : 0)
                  : "memory");
+}
+
+// This thread's arrival, once its cp.async so far are complete.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Waits for the phase of the given parity to complete, for at most `limit` of
@@ -68,17 +73,8 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
     return done;
 }
 
-// Box (x, y, z, w) of a tensor map into shared memory, counted on bar.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, int w, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-                 : "memory");
-}
-
-// This thread's shared-memory writes, made visible to bulk copies and MMAs.
+// This thread's shared-memory writes, (and those it has waited for) made visible
+// to the tensor core's reads.
 __device__ __forceinline__ void fence_async_smem()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -104,35 +100,54 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, bool b_mn_major, int
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// A descriptor as its two halves: steps inside an operand change the low one
+// alone, and stay 32-bit adds.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+};
+
+// The products of one thread of the calling warp (lead != 0), which is one
+// predicate: the warp stays together and keeps the operands in its uniform
+// registers. A branch around the instruction made each product cost some 50 ns.
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t astep, Desc b, uint32_t bstep,
+                                       uint32_t idesc, uint32_t acc, uint32_t lead)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "setp.ne.b32 q, %7, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+                 "r"(a.lo + astep), "r"(a.hi), "r"(b.lo + bstep), "r"(b.hi), "r"(idesc), "r"(acc), "r"(lead)
                  : "memory");
 }
 
 // The same on 8-bit operands (32 along K).
-__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, Desc a, uint32_t astep, Desc b, uint32_t bstep,
+                                          uint32_t idesc, uint32_t acc, uint32_t lead)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "setp.ne.b32 q, %7, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+                 "r"(a.lo + astep), "r"(a.hi), "r"(b.lo + bstep), "r"(b.hi), "r"(idesc), "r"(acc), "r"(lead)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// A read from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t bstep, uint32_t idesc,
+                                       uint32_t acc, uint32_t lead)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "setp.ne.b32 q, %6, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b.lo + bstep), "r"(b.hi), "r"(idesc), "r"(acc), "r"(lead)
                  : "memory");
 }
 
-// Every MMA this thread issued so far, complete, arrives once on bar.
-__device__ __forceinline__ void tc_commit(uint32_t bar)
+// Every MMA the leading thread issued so far, complete, arrives once on bar.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(lead)
                  : "memory");
 }
 

@@ -19,10 +19,12 @@
 // directly.
 //
 // Both products are tcgen05.mma of 128 rows and 128 keys. The warps:
-//  * one walks the run and copies keys, one copies values, by the box of a
-//    page's rows (cp.async.bulk.tensor, swizzled) into a ring, two slots per
-//    128 keys; what lies behind a segment's keys, and bad pages, is filled with
-//    zeros by a box outside the map;
+//  * one walks the run and copies keys, one copies values, row by row into a
+//    ring, two slots per 128 keys, in the products' swizzled layout; what lies
+//    behind a segment's keys, and bad pages, is filled with zeros. The copies
+//    are cp.async, 16 bytes a lane: by bulk tensor copies, a box per page and
+//    128 bytes, the issue of the boxes set the pace (70 to 110 ns a box and
+//    warp: 1.15 us per 128 8-bit keys in pages of 24, where the bytes take 0.2);
 //  * one thread issues S = Q K^T (both from shared memory) into one of two
 //    accumulators, one tile ahead and across segments, and O += P V with P
 //    read from tensor memory, where it takes S's place;
@@ -65,7 +67,7 @@ constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
 constexpr int kTiles = 16;      // tiles that are
-constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 2000000ull;
+constexpr unsigned long long kSegWaitNs = 2000000000ull;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
@@ -80,22 +82,16 @@ struct Cfg {
     static constexpr int SLOT = NSUB * SUB;                   // 128 keys (or values), 16 bits
     static constexpr int Q1 = F8 ? 2 * SUB : SLOT, Q = TWO ? 2 * Q1 : Q1; // 128 rows of q; all of them
     static constexpr int KV_BYTES = F8 ? (TWO ? 64 : 96) * 1024 : (TWO ? 4 : 5) * (D == 128 ? 1 : 2) * SLOT; // the ring of copies
-    static constexpr int MAX_SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
+    static constexpr int SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
+    static constexpr int ROWB = F8 ? D : 2 * D, CPR = ROWB / 16; // bytes, 16-byte chunks of a key
     static constexpr int JOIN = 2 * kGroup * 64;
-    static constexpr int BARS = 2 * MAX_SLOTS + 2 * NV + 6 + 3 * kRing + 2;
+    static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 2;
     static constexpr int SMEM = 1024 + Q + KV_BYTES + NV * SLOT + JOIN + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
     // copies run ahead of the softmax by the ring's tiles, 8-bit ones by NV more and the
     // one in between: its entries live that long, those of tail tiles without the ring
-    static_assert(MAX_SLOTS / 2 + NV + 2 <= kTiles && (F8 ? NV + 1 : MAX_SLOTS / 2 + 1) <= kRing, "ring entries");
-};
-
-struct TcArgs {
-    AttnProblem p;
-    int box;   // rows of a copy's box: the largest power of two up to 64 that divides the page
-    int pitch; // bytes from row to row of an 8-bit slot: a box starts on 128 bytes, so a box
-               // of one 64-byte row leaves the other 64 empty
+    static_assert(SLOTS / 2 + NV + 2 <= kTiles && (F8 ? NV + 1 : SLOTS / 2 + 1) <= kRing, "ring entries");
 };
 
 // What a CTA's warps need of a segment (nt = 0: the run has ended).
@@ -147,11 +143,9 @@ __device__ __forceinline__ uint32_t op_off(int r, int c)
 
 template <int D, int KV, int MT>
 __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
-    attn_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap)
+    attn_kernel(const __grid_constant__ AttnProblem p)
 {
     using C = Cfg<D, KV, MT>;
-    const AttnProblem &p = a.p;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ long long s_scan[4], s_first;
@@ -166,13 +160,13 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ int s_acc[2];                             // a group's first product of a segment adds to O
     uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sQ = smem_u32(smem), sKV = sQ + C::Q, sV = sKV + C::KV_BYTES, sJoin = sV + C::NV * C::SLOT;
-    const uint32_t bFull = sJoin + C::JOIN, bEmpty = bFull + 8 * C::MAX_SLOTS;
-    const uint32_t bVFull = bEmpty + 8 * C::MAX_SLOTS, bVEmpty = bVFull + 8 * C::NV;
+    const uint32_t bFull = sJoin + C::JOIN, bEmpty = bFull + 8 * C::SLOTS;
+    const uint32_t bVFull = bEmpty + 8 * C::SLOTS, bVEmpty = bVFull + 8 * C::NV;
     const uint32_t bS = bVEmpty + 8 * C::NV, bP = bS + 16, bO = bP + 16;
     const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8;
     // the ring of copies: keys in one slot, values in the next
-    const uint32_t slot_bytes = C::F8 ? kTile * a.pitch : C::SLOT;
-    const int slots = C::F8 ? (a.pitch == D ? C::MAX_SLOTS : C::KV_BYTES / (kTile * 128)) : C::MAX_SLOTS;
+    constexpr uint32_t slot_bytes = kTile * C::ROWB;
+    constexpr int slots = C::SLOTS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.cache.heads, G = p.Hq / Hkv;
 
@@ -180,10 +174,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else if (warp == kKeys && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
-        for (int s = 0; s < C::MAX_SLOTS; ++s) {
-            bar_init(bFull + 8 * s, 1);
+        for (int s = 0; s < C::SLOTS; ++s) {
+            bar_init(bFull + 8 * s, 32); // the lanes of the copying warp
             // read by the products and followed by the value warps; 8-bit keys by the
             // products alone, 8-bit values by the value warps alone
             bar_init(bEmpty + 8 * s, !C::F8 ? 1 + C::VW : s & 1 ? C::VW : 1);
@@ -268,9 +260,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
 
     if (warp == kKeys || warp == kValues) {
         // ---- the run's segments; pages -> slots ------------------------------
-        // Lane x knows piece x of a slot: a box of `box` rows and 128 bytes (all
-        // pieces, for pages of at least 8 slots; the others are looked up when
-        // their turn comes). The pages of the next two tiles are looked up ahead.
+        // Lane x knows rows x, x + 32, x + 64, x + 96 of a slot; the pages of the
+        // next tile are looked up ahead. Lane x then copies chunk x % CPR of row
+        // x / CPR of each group of 32 / CPR rows.
         const bool keys = warp == kKeys;
         Walk walk;
         if (keys && u < u_end) {
@@ -280,20 +272,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             walk.base = s_first;
             walk.rq = s_rq;
         }
-        const uint32_t bytes = C::F8 ? kTile * D : C::SLOT; // of one slot's boxes
-        constexpr int PARTS = C::F8 ? 1 : C::NSUB;          // boxes side by side in a row
-        const int row_bytes = C::F8 ? a.pitch : 128;
-        const int pieces = kTile / a.box * PARTS, near = min(pieces, 32);
+        constexpr int ES = C::F8 ? 1 : 2, RPI = 32 / C::CPR; // rows of one copy instruction
         const int page = p.cache.page, page_up = kTile / page, slot_up = kTile % page;
-        const CUtensorMap *map = keys ? &kmap : &vmap;
-        auto step = [&](int &g, int &s) { // one tile on
-            g += page_up;
-            s += slot_up;
-            if (s >= page) {
-                s -= page;
-                ++g;
-            }
-        };
+        const uint8_t *cache = static_cast<const uint8_t *>(keys ? p.cache.k : p.cache.v) + 16 * (lane % C::CPR);
         Ring ring{keys ? 0 : 1, 0}, seg{0, 0};
         Split split0{}, split1{};
         int i = 0, tails = 0; // tiles, tail tiles so far
@@ -340,16 +321,16 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             if (nt == 0)
                 break;
             const int32_t *table = p.table + (long long)r * p.table_ld;
-            // this lane's box: page index, slot in it, ids of the next tiles
-            const int first = key0 + lane / PARTS * a.box;
-            int pg = first / page, sl = first - pg * page;
-            auto look = [&](int t, int at_page) {
-                return lane < pieces && t < nt && first + t * kTile < end ? table[at_page] : -1;
-            };
-            int pg_next = pg, sl_next = sl;
-            int id0 = look(0, pg);
-            step(pg_next, sl_next);
-            int id1 = look(1, pg_next);
+            const uint8_t *head = cache + h * p.cache.head_stride * ES;
+            // this lane's rows: page index, slot in it, the next tile's page ids
+            int pg[4], sl[4], id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = key0 + lane + 32 * j;
+                pg[j] = key / page;
+                sl[j] = key - pg[j] * page;
+                id[j] = key < end ? table[pg[j]] : -1;
+            }
             if (keys && !walk.whole()) { // a part for join_kernel
                 Split sp;
                 sp.c0 = cta_of(U, walk.item0, ctas);
@@ -365,195 +346,186 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
 #pragma unroll 1
             for (int t = 0; t < nt; ++t, ++i) {
-                int pg2 = pg_next, sl2 = sl_next;
-                step(pg2, sl2);
-                const int id2 = look(t + 2, pg2);
-                // this lane's box; its page is waited for here
-                const bool want = lane < pieces && first + t * kTile < end;
-                const bool good = want && id0 >= 0 && id0 < p.cache.num_pages;
-                const int pid = good ? id0 : p.cache.num_pages; // outside the map: zeros
-                const int slot = good ? sl : 0;
-                if (keys) { // the keys without a page
-                    uint32_t *bad = s_bad[i % kTiles];
-                    if (lane < 4)
-                        bad[lane] = 0;
-                    bool any = __any_sync(~0u, want && !good);
-                    __syncwarp();
-                    if (any && want && !good && lane % PARTS == 0)
-                        for (int k = 0; k < a.box; ++k) {
-                            const int b = lane / PARTS * a.box + k;
-                            atomicOr(&bad[b >> 5], 1u << (b & 31));
-                        }
-                    for (int j = 32 + lane; j < pieces; j += 32) {
-                        const int b = j / PARTS, kb = key0 + t * kTile + b * a.box;
-                        if (kb < end) {
-                            const int id = table[kb / page];
-                            if (id < 0 || id >= p.cache.num_pages) {
-                                any = true;
-                                for (int k = 0; k < a.box; ++k)
-                                    atomicOr(&bad[(b * a.box + k) >> 5], 1u << ((b * a.box + k) & 31));
-                            }
-                        }
+                // these rows' offsets, -1 where there is none; the next ones' pages
+                long long off[4];
+                uint32_t bad[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + t * kTile + lane + 32 * j;
+                    const bool want = key < end, good = want && id[j] >= 0 && id[j] < p.cache.num_pages;
+                    off[j] = good ? (id[j] * p.cache.page_stride + sl[j] * p.cache.slot_stride) * ES : -1;
+                    bad[j] = __ballot_sync(~0u, want && !good);
+                    pg[j] += page_up;
+                    sl[j] += slot_up;
+                    if (sl[j] >= page) {
+                        sl[j] -= page;
+                        ++pg[j];
                     }
-                    if (any)
+                    id[j] = key + kTile < end ? table[pg[j]] : -1;
+                }
+                if (keys && lane < 4) {
+                    const uint32_t b = lane < 2 ? (lane ? bad[1] : bad[0]) : lane == 2 ? bad[2] : bad[3];
+                    s_bad[i % kTiles][lane] = b;
+                    if (b)
                         set_status(p.status, SGQ_STATUS_BAD_INDEX);
-                    __syncwarp();
                 }
                 bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
-                if (!__all_sync(~0u, ok)) {
-                    ok = false;
-                    continue;
-                }
-                const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
-                if (lane == 0)
-                    bar_expect(full, bytes);
                 __syncwarp();
-                // one lane issues all of them: the copy takes its operands from
-                // registers that a warp shares
-#pragma unroll 4
-                for (int x = 0; x < near; ++x) {
-                    const int id = __shfl_sync(~0u, pid, x), s = __shfl_sync(~0u, slot, x);
-                    if (lane == 0)
-                        tma_load_4d(dst + (x % PARTS) * C::SUB + x / PARTS * a.box * row_bytes, map, x % PARTS * 64, s, h, id, full);
-                }
-                for (int x = 32 + lane; x < pieces; x += 32) {
-                    const int b = x / PARTS, kb = key0 + t * kTile + b * a.box;
-                    int id = kb < end ? table[kb / page] : -1;
-                    if (id < 0 || id >= p.cache.num_pages)
-                        id = p.cache.num_pages;
-                    tma_load_4d(dst + (x % PARTS) * C::SUB + b * a.box * row_bytes, map, x % PARTS * 64, kb % page, h, id, full);
-                }
+                const uint32_t dst = sKV + ring.s * slot_bytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll 8
+                    for (int k = 0; k < 32 / RPI; ++k) {
+                        const int row = 32 * j + k * RPI + lane / C::CPR;
+                        const long long o = __shfl_sync(~0u, off[j], k * RPI + lane / C::CPR);
+                        const int c = lane % C::CPR;
+                        uint32_t at; // the swizzle: of 128 bytes, or of 64 with rows of 64
+                        if constexpr (!C::F8)
+                            at = op_off(row, c);
+                        else if constexpr (D == 128)
+                            at = row * 128 + ((c ^ (row & 7)) << 4);
+                        else
+                            at = row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+                        cp_async16_zfill(dst + at, head + max(o, 0ll), o >= 0);
+                    }
+                cp_async_arrive(bFull + 8 * ring.s);
                 ring.step(2, slots);
-                sl = sl_next;
-                pg_next = pg2;
-                sl_next = sl2;
-                id0 = id1;
-                id1 = id2;
             }
         }
         if (keys && lane < 2)
             static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split1 : split0;
+        cp_async_wait_all();
     } else if (warp == kIssuer) {
         // ---- the products ------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
-            Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
-            uint32_t q_ph = 0;
-            int left = 0, nt = 0; // tiles of the segment without scores, all of them
-            bool ended = false;
-            // Whether there is a next tile; its segment is looked up.
-            auto next = [&]() -> bool {
-                if (left == 0 && !ended) {
-                    bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
-                    left = led ? *(volatile int *)&s_seg[seg.s].nt : 0;
-                    seg.step(1, kRing);
-                    ended = left == 0;
-                    nt = -left; // its Q has not been waited for
-                }
-                return !ended;
-            };
-            // The scores of the next tile for group g's rows, into S number buf.
-            auto scores = [&](int g, int buf) {
-                if (nt < 0) {
-                    bar_wait(bQ, q_ph, ok);
-                    q_ph ^= 1;
-                    nt = -nt;
-                }
-                bar_wait(bFull + 8 * kr.s, kr.ph, ok);
-                tc_after();
-                const uint32_t d = tmem + buf * kTile, ka = sKV + kr.s * slot_bytes, qa = sQ + g * C::Q1;
-                const uint64_t dq = op_desc(qa, 16, 1024);
-                if constexpr (C::F8) {
-                    // q's two parts one after the other
-                    const uint64_t dk = op_desc(ka, 16, 8 * a.pitch, a.pitch == 128 ? 2 : 4);
+        constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
+        uint32_t lead = 0; // one lane issues, see mma_ss
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+        Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
+        uint32_t q_ph = 0;
+        int left = 0, nt = 0; // tiles of the segment without scores, all of them
+        bool ended = false;
+        // Whether there is a next tile; its segment is looked up.
+        auto next = [&]() -> bool {
+            if (left == 0 && !ended) {
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+                __syncwarp();
+                left = __all_sync(~0u, led) ? s_seg[seg.s].nt : 0;
+                seg.step(1, kRing);
+                ended = left == 0;
+                nt = -left; // its Q has not been waited for
+            }
+            return !ended;
+        };
+        // The scores of the next tile for group g's rows, into S number buf.
+        auto scores = [&](int g, int buf) {
+            if (nt < 0) {
+                bar_wait(bQ, q_ph, ok);
+                q_ph ^= 1;
+                nt = -nt;
+            }
+            bar_wait(bFull + 8 * kr.s, kr.ph, ok);
+            fence_async_smem(); // the copies' writes, for the product's reads
+            __syncwarp();
+            tc_after();
+            const uint32_t d = tmem + buf * kTile, ka = sKV + kr.s * slot_bytes;
+            const Desc dq(op_desc(sQ + g * C::Q1, 16, 1024));
+            if constexpr (C::F8) {
+                // q's two parts one after the other
+                const Desc dk(op_desc(ka, 16, 8 * D, D == 128 ? 2 : 4));
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        mma_ss_f8(d, dq + 2 * k, dk + 2 * k, idS, k > 0);
-                        mma_ss_f8(d, dq + (C::SUB >> 4) + 2 * k, dk + 2 * k, idS, 1);
-                    }
-                } else {
-                    const uint64_t dk = op_desc(ka, 16, 1024);
+                for (int k = 0; k < D / 32; ++k) {
+                    mma_ss_f8(d, dq, 2 * k, dk, 2 * k, idS, k > 0, lead);
+                    mma_ss_f8(d, dq, (C::SUB >> 4) + 2 * k, dk, 2 * k, idS, 1, lead);
+                }
+            } else {
+                const Desc dk(op_desc(ka, 16, 1024));
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t st = (uint64_t)(((k >> 2) * C::SUB + (k & 3) * 32) >> 4);
-                        mma_ss(d, dq + st, dk + st, idS, k > 0);
-                    }
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t st = ((k >> 2) * C::SUB + (k & 3) * 32) >> 4;
+                    mma_ss(d, dq, st, dk, st, idS, k > 0, lead);
                 }
-                tc_commit(bS + 8 * buf);
-                if (!C::TWO || g == 1) {
-                    tc_commit(bEmpty + 8 * kr.s);
-                    if (--left == 0)
-                        tc_commit(bQFree);
-                    kr.step(2, slots);
-                }
-            };
-            // Tile i's product with the values into O number buf.
-            auto values = [&](int i, int buf, uint32_t p_ph, bool begun) {
-                const uint32_t vfull = C::F8 ? bVFull + 8 * (i & 1) : bFull + 8 * vr.s;
-                bar_wait(vfull, C::F8 ? (i >> 1) & 1 : vr.ph, ok);
-                bar_wait(bP + 8 * buf, p_ph, ok);
-                tc_after();
-                const uint32_t add = begun || *(volatile int *)&s_acc[buf];
-                const uint32_t va = C::F8 ? sV + (i & 1) * C::SLOT : sKV + vr.s * slot_bytes;
-                const uint64_t dv = op_desc(va, C::SUB, 1024);
+            }
+            tc_commit(bS + 8 * buf, lead);
+            if (!C::TWO || g == 1) {
+                tc_commit(bEmpty + 8 * kr.s, lead);
+                if (--left == 0)
+                    tc_commit(bQFree, lead);
+                kr.step(2, slots);
+            }
+        };
+        // Tile i's product with the values into O number buf.
+        auto values = [&](int i, int buf, uint32_t p_ph, bool begun) {
+            const uint32_t vfull = C::F8 ? bVFull + 8 * (i & 1) : bFull + 8 * vr.s;
+            bar_wait(vfull, C::F8 ? (i >> 1) & 1 : vr.ph, ok);
+            bar_wait(bP + 8 * buf, p_ph, ok);
+            if (!C::F8)
+                fence_async_smem();
+            __syncwarp();
+            tc_after();
+            const uint32_t add = begun || *(volatile int *)&s_acc[buf];
+            const Desc dv(op_desc(C::F8 ? sV + (i & 1) * C::SLOT : sKV + vr.s * slot_bytes, C::SUB, 1024));
+            const uint32_t o = tmem + kColO + buf * 128, w = tmem + buf * kTile;
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + kColO + buf * 128, tmem + buf * kTile + 8 * k, dv + (uint64_t)((k * 2048) >> 4), idO, add | (k > 0));
-                tc_commit(bO + 8 * buf);
-                if (!C::TWO || buf == 1) {
-                    tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s);
-                    vr.step(2, slots);
-                }
-            };
-            int i = 0, t = 0; // tile, its number in its segment
-            bool more = next();
-            if (more) {
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(o, w + 8 * k, dv, (k * 2048) >> 4, idO, add | (k > 0), lead);
+            tc_commit(bO + 8 * buf, lead);
+            if (!C::TWO || buf == 1) {
+                tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s, lead);
+                vr.step(2, slots);
+            }
+        };
+        int i = 0, t = 0; // tile, its number in its segment
+        bool more = next();
+        int nt_i = abs(nt); // its segment's tiles
+        // The tiles' products, scores one tile ahead. Into the next segment only
+        // if its Q is there (with rows for both groups: never), else after the
+        // values. The first tile has no values before it.
+        for (int step = -1; step < 0 || more; ++step) {
+            if (step < 0) {
+                if (!more)
+                    break;
                 scores(0, 0);
                 if constexpr (C::TWO)
                     scores(1, 1);
+                continue;
             }
-            int nt_i = nt; // its segment's tiles
-            while (more) {
-                more = next();
-                const bool crosses = more && nt < 0; // into the next segment
-                if constexpr (C::TWO) {
-                    values(i, 0, i & 1, t > 0);
-                    if (more && !crosses)
-                        scores(0, 0);
-                    values(i, 1, i & 1, t > 0);
-                    if (more) {
-                        if (crosses)
-                            scores(0, 0);
-                        scores(1, 1);
-                    }
-                } else {
-                    // one tile ahead, but not if the next segment's Q is waited for
-                    const bool ahead = more && (!crosses || bar_test(bQ, q_ph));
-                    if (ahead)
-                        scores(0, (i + 1) & 1);
-                    values(i, i & 1, (i >> 1) & 1, t >= 2);
-                    if (more && !ahead)
-                        scores(0, (i + 1) & 1);
-                }
-                ++i;
-                if (++t == nt_i) {
-                    t = 0;
-                    nt_i = nt;
-                }
-            }
-            // every product is complete before the tensor memory is freed
-            bool done = true;
+            more = next();
+            const bool crosses = more && nt < 0;
+            const bool ahead = more && (!crosses || (!C::TWO && __all_sync(~0u, bar_test(bQ, q_ph))));
             if constexpr (C::TWO) {
-                for (int b = 0; b < 2 && i > 0; ++b)
-                    bar_wait(bO + 8 * b, (i - 1) & 1, done);
+                values(i, 0, i & 1, t > 0);
+                if (ahead)
+                    scores(0, 0);
+                values(i, 1, i & 1, t > 0);
+                if (more && !ahead)
+                    scores(0, 0);
+                if (more)
+                    scores(1, 1);
             } else {
-                if (i >= 2)
-                    bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, done);
-                if (i >= 1)
-                    bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, done);
+                if (ahead)
+                    scores(0, (i + 1) & 1);
+                values(i, i & 1, (i >> 1) & 1, t >= 2);
+                if (more && !ahead)
+                    scores(0, (i + 1) & 1);
             }
-            ok = ok && done;
+            ++i;
+            if (++t == nt_i) {
+                t = 0;
+                nt_i = abs(nt);
+            }
         }
+        // every product is complete before the tensor memory is freed
+        bool done = true;
+        if constexpr (C::TWO) {
+            for (int b = 0; b < 2 && i > 0; ++b)
+                bar_wait(bO + 8 * b, (i - 1) & 1, done);
+        } else {
+            if (i >= 2)
+                bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, done);
+            if (i >= 1)
+                bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, done);
+        }
+        ok = ok && done;
         __syncwarp();
     } else if (warp >= kQ && warp < C::kV) {
         // ---- Q -----------------------------------------------------------
@@ -676,8 +648,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     for (int k = 0; k < M; ++k) {
                         const int idx = ct + k * VT, row = idx / (D / 16), c = idx % (D / 16);
                         // the copies' swizzle: of 128 bytes, or of 64 with rows of 64
-                        const int x = c ^ (a.pitch == 128 ? row & 7 : (row >> 1) & 3);
-                        v[k] = *reinterpret_cast<const uint4 *>(src + row * a.pitch + 16 * x);
+                        const int x = c ^ (D == 128 ? row & 7 : (row >> 1) & 3);
+                        v[k] = *reinterpret_cast<const uint4 *>(src + row * D + 16 * x);
                     }
 #pragma unroll
                     for (int k = 0; k < M; ++k) {
@@ -1036,17 +1008,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         }
     }
     tc_before();
-    if (__syncthreads_or(!ok || !led)) {
-        // a wait ran out: copies that nothing waited for may be on their way
-        // still, and take microseconds
+    if (!ok || !led)
         set_status(p.status, SGQ_STATUS_TIMEOUT);
-        unsigned long long t0, t;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-        do
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        while (t - t0 < kDrainNs);
-        __syncthreads();
-    }
+    __syncthreads();
     if (warp == kIssuer)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
@@ -1054,7 +1018,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
 // Joins the parts of the items that several CTAs worked on, in key order. The
 // CTAs of an item share its rows here too: CTA c0 + x takes rows x, x + parts,
 // ... A row is read by as many of the CTA's warps as there are rows too few.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem p, int MT)
@@ -1151,59 +1115,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
     }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder of tensor maps, looked up once.
-EncodeTiled encoder()
-{
-    static const EncodeTiled f = [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<EncodeTiled>(fn);
-    }();
-    return f;
-}
-
-// (element, slot, head, page) of the cache; a box is 128 bytes of a row (64
-// where the row has no more) times `box` slots of one page and head. A
-// dimension of one entry has no stride of its own: any valid one will do.
-bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box, int pitch)
-{
-    const bool f8 = c.type == SGQ_TYPE_E4M3;
-    const int es = f8 ? 1 : 2, inner = std::min(c.dim, 128 / es);
-    const cuuint64_t row = (cuuint64_t)c.dim * es;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {c.page > 1 ? (cuuint64_t)c.slot_stride * es : row,
-                                   c.heads > 1 ? (cuuint64_t)c.head_stride * es : row,
-                                   c.num_pages > 1 ? (cuuint64_t)c.page_stride * es : row};
-    const cuuint32_t boxes[4] = {(cuuint32_t)inner, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return encoder()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes,
-                     ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     pitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int KV, int MT>
 cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
 {
     using C = Cfg<D, KV, MT>;
-    TcArgs a;
-    a.p = p;
-    a.box = 1;
-    while (a.box < 64 && p.cache.page % (2 * a.box) == 0)
-        a.box *= 2;
-    a.pitch = C::F8 && a.box > 1 ? D : 128;
-    CUtensorMap kmap, vmap;
-    if (!encoder())
-        return cudaErrorNotSupported;
-    if (!encode(&kmap, p.cache, p.cache.k, a.box, a.pitch) || !encode(&vmap, p.cache, p.cache.v, a.box, a.pitch))
-        return cudaErrorInvalidValue;
-    cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, a, kmap, vmap);
+    const cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);
