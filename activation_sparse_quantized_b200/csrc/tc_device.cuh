@@ -4,6 +4,8 @@
 
 #include "sgq_device.cuh"
 
+#include <cuda.h>
+
 namespace sgq {
 
 namespace {
@@ -19,6 +21,34 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// This thread's arrival, and `bytes` more to come from bulk copies.
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+// Box (x, y, z, w) of a tensor map into shared memory, counted on bar; by one
+// thread of the calling warp (lead != 0).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, uint32_t bar, uint32_t lead)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+                 "@q cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(lead)
+                 : "memory");
+}
+
+// One lane of a warp that is together: 1 there, 0 in the others.
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(lead));
+    return lead;
 }
 
 // 16 bytes into shared memory, or zeros.

@@ -66,8 +66,9 @@ constexpr int kSoftWarps = 8, kKeys = 8, kValues = 9, kIssuer = 10, kQ = 11; // 
 constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
+constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
-constexpr unsigned long long kSegWaitNs = 2000000000ull;
+constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 400000000ull;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
@@ -143,7 +144,8 @@ __device__ __forceinline__ uint32_t op_off(int r, int c)
 
 template <int D, int KV, int MT>
 __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
-    attn_kernel(const __grid_constant__ AttnProblem p)
+    attn_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const int box)
 {
     using C = Cfg<D, KV, MT>;
     extern __shared__ uint8_t smem_raw[];
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else if (warp == kKeys && lane == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
-            bar_init(bFull + 8 * s, 32); // the lanes of the copying warp
+            bar_init(bFull + 8 * s, box ? 1 : 32); // one bulk copy's thread, or the lanes of a warp
             // read by the products and followed by the value warps; 8-bit keys by the
             // products alone, 8-bit values by the value warps alone
             bar_init(bEmpty + 8 * s, !C::F8 ? 1 + C::VW : s & 1 ? C::VW : 1);
@@ -274,6 +276,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         }
         constexpr int ES = C::F8 ? 1 : 2, RPI = 32 / C::CPR; // rows of one copy instruction
         const int page = p.cache.page, page_up = kTile / page, slot_up = kTile % page;
+        constexpr int PARTS = C::F8 ? 1 : C::NSUB; // boxes side by side in a row
+        const int pieces = box ? kTile / box * PARTS : 0;
+        const CUtensorMap *map = keys ? &kmap : &vmap;
+        const uint32_t lead = elect_lane();
         const uint8_t *cache = static_cast<const uint8_t *>(keys ? p.cache.k : p.cache.v) + 16 * (lane % C::CPR);
         Ring ring{keys ? 0 : 1, 0}, seg{0, 0};
         Split split0{}, split1{};
@@ -321,16 +327,6 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             if (nt == 0)
                 break;
             const int32_t *table = p.table + (long long)r * p.table_ld;
-            const uint8_t *head = cache + h * p.cache.head_stride * ES;
-            // this lane's rows: page index, slot in it, the next tile's page ids
-            int pg[4], sl[4], id[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = key0 + lane + 32 * j;
-                pg[j] = key / page;
-                sl[j] = key - pg[j] * page;
-                id[j] = key < end ? table[pg[j]] : -1;
-            }
             if (keys && !walk.whole()) { // a part for join_kernel
                 Split sp;
                 sp.c0 = cta_of(U, walk.item0, ctas);
@@ -343,6 +339,76 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     split1 = sp;
                 else
                     split0 = sp;
+            }
+            if (box) {
+                // Lane x looks up piece x of a slot: rows of one page, 128 bytes.
+                // The next two tiles' pages are looked up ahead.
+                const int first = key0 + lane / PARTS * box;
+                int pg = first / page, sl = first - pg * page;
+                auto look = [&](int t, int at_page) {
+                    return lane < pieces && t < nt && first + t * kTile < end ? table[at_page] : -1;
+                };
+                auto step = [&](int &g, int &s) { // one tile on
+                    g += page_up;
+                    s += slot_up;
+                    if (s >= page) {
+                        s -= page;
+                        ++g;
+                    }
+                };
+                int pg_next = pg, sl_next = sl;
+                int id0 = look(0, pg);
+                step(pg_next, sl_next);
+                int id1 = look(1, pg_next);
+#pragma unroll 1
+                for (int t = 0; t < nt; ++t, ++i) {
+                    int pg2 = pg_next, sl2 = sl_next;
+                    step(pg2, sl2);
+                    const int id2 = look(t + 2, pg2);
+                    const bool want = lane < pieces && first + t * kTile < end;
+                    const bool good = want && id0 >= 0 && id0 < p.cache.num_pages;
+                    const int pid = good ? id0 : p.cache.num_pages; // outside the map: zeros
+                    const int slot = good ? sl : 0;
+                    const uint32_t lost = __ballot_sync(~0u, want && !good);
+                    if (keys && lane < 4) { // the keys without a page, 32 a lane
+                        uint32_t b = 0;
+                        if (lost) {
+                            for (int k = 0; k < 32; ++k)
+                                b |= ((lost >> ((32 * lane + k) / box * PARTS)) & 1) << k;
+                            set_status(p.status, SGQ_STATUS_BAD_INDEX);
+                        }
+                        s_bad[i % kTiles][lane] = b;
+                    }
+                    bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
+                    __syncwarp();
+                    const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
+                    if (lane == 0)
+                        bar_expect(full, kTile * C::ROWB);
+                    __syncwarp();
+#pragma unroll 4
+                    for (int x = 0; x < pieces; ++x) {
+                        const int at = __shfl_sync(~0u, pid, x), s = __shfl_sync(~0u, slot, x);
+                        tma_load_4d(dst + x % PARTS * C::SUB + x / PARTS * box * min(C::ROWB, 128), map, x % PARTS * 64, s, h, at,
+                                    full, lead);
+                    }
+                    ring.step(2, slots);
+                    sl = sl_next;
+                    pg_next = pg2;
+                    sl_next = sl2;
+                    id0 = id1;
+                    id1 = id2;
+                }
+                continue;
+            }
+            const uint8_t *head = cache + h * p.cache.head_stride * ES;
+            // this lane's rows: page index, slot in it, the next tile's page ids
+            int pg[4], sl[4], id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = key0 + lane + 32 * j;
+                pg[j] = key / page;
+                sl[j] = key - pg[j] * page;
+                id[j] = key < end ? table[pg[j]] : -1;
             }
 #pragma unroll 1
             for (int t = 0; t < nt; ++t, ++i) {
@@ -395,11 +461,19 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         if (keys && lane < 2)
             static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split1 : split0;
         cp_async_wait_all();
+        if (box && !__all_sync(~0u, ok)) {
+            // a wait ran out: bulk copies that nothing waited for may be on their
+            // way still, and take microseconds
+            unsigned long long t0, t;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+            do
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            while (t - t0 < kDrainNs);
+        }
     } else if (warp == kIssuer) {
         // ---- the products ------------------------------------------------
         constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
-        uint32_t lead = 0; // one lane issues, see mma_ss
-        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+        const uint32_t lead = elect_lane(); // it issues, see mma_ss
         Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
         uint32_t q_ph = 0;
         int left = 0, nt = 0; // tiles of the segment without scores, all of them
@@ -1115,11 +1189,62 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
     }
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps, looked up once.
+EncodeTiled encoder()
+{
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<EncodeTiled>(fn);
+    }();
+    return f;
+}
+
+// (element, slot, head, page) of the cache; a box is 128 bytes of a row (64
+// where the row has no more) times `box` slots of one page and head. A
+// dimension of one entry has no stride of its own: any valid one will do.
+bool encode(CUtensorMap *map, const sgq_cache &c, void *base, int box)
+{
+    const bool f8 = c.type == SGQ_TYPE_E4M3;
+    const int es = f8 ? 1 : 2, inner = std::min(c.dim, 128 / es);
+    const cuuint64_t row = (cuuint64_t)c.dim * es;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {c.page > 1 ? (cuuint64_t)c.slot_stride * es : row,
+                                   c.heads > 1 ? (cuuint64_t)c.head_stride * es : row,
+                                   c.num_pages > 1 ? (cuuint64_t)c.page_stride * es : row};
+    const cuuint32_t boxes[4] = {(cuuint32_t)inner, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return encoder()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes,
+                     ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int KV, int MT>
 cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
 {
     using C = Cfg<D, KV, MT>;
-    const cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, p);
+    // Bulk copies where a box, the largest power of two up to 64 slots that
+    // divides the page, has kBoxBytes at least: 84 us against 88 on 11 requests
+    // of up to 60000 8-bit keys in pages of 24 (boxes of 512 bytes), 72 against
+    // 83 on 24 ragged ones in pages of 32 (boxes of 4 KB).
+    int box = 1;
+    while (box < 64 && p.cache.page % (2 * box) == 0)
+        box *= 2;
+    CUtensorMap kmap{}, vmap{};
+    if (box * std::min(C::ROWB, 128) < kBoxBytes)
+        box = 0;
+    else if (!encoder())
+        return cudaErrorNotSupported;
+    else if (!encode(&kmap, p.cache, p.cache.k, box) || !encode(&vmap, p.cache, p.cache.v, box))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, p, kmap, vmap, box);
     if (e != cudaSuccess)
         return e;
     return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);
