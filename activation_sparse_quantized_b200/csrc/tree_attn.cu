@@ -38,11 +38,13 @@
 //    values are made fp16 (exact): weights of 8 bits would lose a long row's
 //    tail.
 // Row tiles (MT): with 256 rows each group has 128 of them and both see every
-// key. With fewer the groups take the tiles of keys in turn (a segment of one
-// tile is one group's alone), and 32 or 64 rows are laid into the 128 several
-// times: copy c takes part c of the keys, its P zero elsewhere, so that all the
-// softmax warps share the exponentials of a few rows. What the copies and
-// groups summed over their keys is joined at the segment's end.
+// key. With 128 the groups take the tiles of keys in turn (a segment of one
+// tile is one group's alone), and their O are joined at the segment's end. With
+// 32 they do too, and the rows are laid into Q's 128 four times, so that each
+// warp finds the scores of all of them in its lanes and takes a quarter of the
+// keys: the warps agree on the rows' maxima and put their quarters of P side by
+// side in shared memory, where the product reads it (its rows from 32 on are
+// whatever lies there, and so are those of O).
 //
 // Every wait on a barrier is bounded by 0.2 s; one that runs out sets
 // SGQ_STATUS_TIMEOUT, the thread waits for no data any more and the kernel runs
@@ -73,22 +75,23 @@ constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 400000000ull
 template <int D_, int KV, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_;
-    static constexpr bool F8 = KV == SGQ_TYPE_E4M3, TWO = MT == 256;
+    static constexpr bool F8 = KV == SGQ_TYPE_E4M3, TWO = MT == 256, FEW = MT == 32;
     static constexpr int QW = F8 && !TWO ? 1 : 2, VW = !F8 ? 1 : TWO ? 2 : 4; // warps for Q, for the values read
     static constexpr int kV = kQ + QW, THREADS = 32 * (kV + VW);
-    static constexpr int ROWS = TWO ? 128 : MT;               // of a group
-    static constexpr int COPIES = 128 / ROWS, NCH = 4 / COPIES; // copies of the rows, 32-key chunks of each
+    static constexpr int ROWS = FEW ? 32 : 128;               // of a group
+    static constexpr int COPIES = 128 / ROWS;                 // of the rows, in Q
     static constexpr int SUB = kTile * 128;                   // 128 rows x 128 bytes, swizzled
     static constexpr int NSUB = D / 64;
     static constexpr int SLOT = NSUB * SUB;                   // 128 keys (or values), 16 bits
     static constexpr int Q1 = F8 ? 2 * SUB : SLOT, Q = TWO ? 2 * Q1 : Q1; // 128 rows of q; all of them
+    static constexpr int P1 = FEW ? ROWS * 256 : 0, P = 2 * P1; // P of a group in shared memory
     static constexpr int KV_BYTES = F8 ? (TWO ? 64 : 96) * 1024 : (TWO ? 4 : 5) * (D == 128 ? 1 : 2) * SLOT; // the ring of copies
     static constexpr int SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
     static constexpr int ROWB = F8 ? D : 2 * D, CPR = ROWB / 16; // bytes, 16-byte chunks of a key
-    static constexpr int JOIN = 2 * kGroup * 64;
+    static constexpr int OUT1 = 32 * 64, OUT = (FEW ? 2 : 8) * OUT1; // a writing warp's 32 rows x 16 columns
     static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 2;
-    static constexpr int SMEM = 1024 + Q + KV_BYTES + NV * SLOT + JOIN + BARS * 8;
+    static constexpr int SMEM = 1024 + Q + P + KV_BYTES + NV * SLOT + OUT + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
     // copies run ahead of the softmax by the ring's tiles, 8-bit ones by NV more and the
     // one in between: its entries live that long, those of tail tiles without the ring
@@ -154,15 +157,15 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ int s_r;
     __shared__ Request s_rq;
     __shared__ Seg s_seg[kRing];
-    __shared__ float s_m[2 * C::COPIES][C::ROWS], s_l[2 * C::COPIES][C::ROWS];
-    __shared__ long long s_row[2][C::ROWS]; // where a row's output goes
+    __shared__ float s_m[2][C::COPIES][C::ROWS], s_l[2][C::COPIES][C::ROWS]; // by group and copy
+    __shared__ float s_mx[C::FEW ? 4 : 1][C::COPIES][C::FEW ? 32 : 1];       // a tile's maxima, by group and turn
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
     __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
     __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
     __shared__ int s_acc[2];                             // a group's first product of a segment adds to O
     uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    const uint32_t sQ = smem_u32(smem), sKV = sQ + C::Q, sV = sKV + C::KV_BYTES, sJoin = sV + C::NV * C::SLOT;
-    const uint32_t bFull = sJoin + C::JOIN, bEmpty = bFull + 8 * C::SLOTS;
+    const uint32_t sQ = smem_u32(smem), sP = sQ + C::Q, sKV = sP + C::P, sV = sKV + C::KV_BYTES, sOut = sV + C::NV * C::SLOT;
+    const uint32_t bFull = sOut + C::OUT, bEmpty = bFull + 8 * C::SLOTS;
     const uint32_t bVFull = bEmpty + 8 * C::SLOTS, bVEmpty = bVFull + 8 * C::NV;
     const uint32_t bS = bVEmpty + 8 * C::NV, bP = bS + 16, bO = bP + 16;
     const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8;
@@ -538,10 +541,17 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             tc_after();
             const uint32_t add = begun || *(volatile int *)&s_acc[buf];
             const Desc dv(op_desc(C::F8 ? sV + (i & 1) * C::SLOT : sKV + vr.s * slot_bytes, C::SUB, 1024));
-            const uint32_t o = tmem + kColO + buf * 128, w = tmem + buf * kTile;
+            const uint32_t o = tmem + kColO + buf * 128;
+            if constexpr (C::FEW) {
+                const Desc dp(op_desc(sP + buf * C::P1, 16, 1024));
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(o, w + 8 * k, dv, (k * 2048) >> 4, idO, add | (k > 0), lead);
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ss(o, dp, ((k >> 2) * C::ROWS * 128 + (k & 3) * 32) >> 4, dv, (k * 2048) >> 4, idO, add | (k > 0), lead);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(o, tmem + buf * kTile + 8 * k, dv, (k * 2048) >> 4, idO, add | (k > 0), lead);
+            }
             tc_commit(bO + 8 * buf, lead);
             if (!C::TWO || buf == 1) {
                 tc_commit(C::F8 ? bVEmpty + 8 * (i & 1) : bEmpty + 8 * vr.s, lead);
@@ -794,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     } else {
         // ---- the softmax -------------------------------------------------
         const int grp = warp >> 2, wq = warp & 3;
-        const int quad = wq / (C::ROWS / 32), row = (wq % (C::ROWS / 32)) * 32 + lane; // copy, row of the group's
+        const int quad = C::FEW ? wq : 0, row = C::FEW ? lane : wq * 32 + lane; // copy, row of the group's
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t tS = tmem + grp * kTile + lanes, tO = tmem + kColO + grp * 128 + lanes;
         const int gtid = tid & (kGroup - 1);
@@ -840,40 +850,30 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 const uint32_t *bad = s_bad[(i0 + t) % kTiles];
                 const bool is_tail = t >= sg.first_tail;
                 const bool masked = is_tail || (bad[0] | bad[1] | bad[2] | bad[3]);
-                // the keys of this copy's chunk c that the row sees
+                // the keys of the tile's chunk c that the row sees
                 auto seen = [&](int c) {
-                    const int ch = quad * C::NCH + c;
-                    return (uint32_t)visible(p, rq, tok_i, first, kt + 32 * ch, sg.end) & ~bad[ch];
+                    return (uint32_t)visible(p, rq, tok_i, first, kt + 32 * c, sg.end) & ~bad[c];
                 };
-                if (warp_live) {
-                    uint32_t s[32];
-                    auto chunk = [&](int c) { // its scores, unseen keys' at -infinity
-                        tmem_ld32(tS + 32 * (quad * C::NCH + c), s);
-                        tmem_ld_wait(s);
-                        if (masked) {
-                            const uint32_t vis = seen(c);
+                auto mask = [&](uint32_t *s, int c) { // unseen keys' scores to -infinity
+                    const uint32_t vis = seen(c);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((vis >> e) & 1))
-                                    s[e] = 0xff800000u;
-                        }
-                    };
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < C::NCH; ++c) {
-                        chunk(c);
+                    for (int e = 0; e < 32; ++e)
+                        s[e] = (vis >> e) & 1 ? s[e] : 0xff800000u;
+                };
+                auto highest = [](const uint32_t *s, float *mx) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor;
-                    // the reference moves for the first keys seen, and when outgrown
+                    for (int e = 0; e < 32; ++e)
+                        mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+                };
+                // The reference moves for the first keys seen, and when outgrown;
+                // O (by the warp that has its lanes) and l with it.
+                auto refer = [&](float top) {
                     const bool grow = top > m + kGrowth;
                     if (__any_sync(~0u, grow)) {
                         const float corr = grow ? exp2_fast(m - top) : 1.0f;
                         m = grow ? top : m;
                         l *= corr;
-                        if (t >= dt) { // this group's last product is done: S was issued after it
+                        if (t >= dt && quad == 0) { // this group's last product is done: S was issued after it
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t o[16];
@@ -885,37 +885,72 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m; // nothing seen yet
-                    // The weights are rounded to the values' type for the product
-                    // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
-                    // small ones, 2^-25); their sum l is of the unrounded ones.
-                    float2 sum[2] = {};
-#pragma unroll 1
-                    for (int c = 0; c < C::NCH; ++c) {
-                        if (C::NCH > 1)
-                            chunk(c);
-                        uint32_t w[16];
+                    return m == -INFINITY ? 0.0f : m; // nothing seen yet
+                };
+                // The weights are rounded to the values' type for the product
+                // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
+                // small ones, 2^-25); their sum l is of the unrounded ones.
+                auto weigh = [&](const uint32_t *s, float ref, uint32_t *w, float2 *sum) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 x = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                             make_float2(factor, factor), make_float2(-ref, -ref));
-                            x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
-                            w[e / 2] = pack2<C::F8>(x.x, x.y);
-                        }
-                        tmem_st16(tS + 16 * (quad * C::NCH + c), w); // over scores already read
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                         make_float2(factor, factor), make_float2(-ref, -ref));
+                        x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+                        w[e / 2] = pack2<C::F8>(x.x, x.y);
                     }
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
-                    if constexpr (C::COPIES > 1) {
-                        const uint32_t z[16] = {};
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float2 sum[2] = {};
+                if constexpr (C::FEW) {
+                    uint32_t s[32], w[16];
+                    tmem_ld32(tS + 32 * quad, s);
+                    tmem_ld_wait(s);
+                    if (masked)
+                        mask(s, quad);
+                    highest(s, mx);
+                    s_mx[2 * grp + s_ph][quad][lane] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    named_sync<kGroup>(2 + grp);
+                    float top = s_mx[2 * grp + s_ph][0][lane];
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b / C::NCH != quad)
-                                tmem_st16(tS + 16 * b, z);
+                    for (int c = 1; c < 4; ++c)
+                        top = fmaxf(top, s_mx[2 * grp + s_ph][c][lane]);
+                    const float ref = refer(top * factor);
+                    weigh(s, ref, w, sum);
+                    uint8_t *dst = smem + (sP - sQ) + grp * C::P1 + (quad >> 1) * C::ROWS * 128 + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(dst + ((((quad & 1) * 4 + c) ^ (row & 7)) << 4)) =
+                            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    fence_async_smem();
+                } else if (warp_live) {
+                    // twice over the scores; masked ones go back for the second time
+                    uint32_t s[32];
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(tS + 32 * c, s);
+                        tmem_ld_wait(s);
+                        if (masked) {
+                            mask(s, c);
+                            tmem_st32(tS + 32 * c, s);
+                        }
+                        highest(s, mx);
+                    }
+                    if (masked)
+                        tmem_st_wait();
+                    const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(tS + 32 * c, s);
+                        tmem_ld_wait(s);
+                        uint32_t w[16];
+                        weigh(s, ref, w, sum);
+                        tmem_st16(tS + 16 * c, w); // over scores already read
                     }
                     tmem_st_wait();
                 }
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
                 if (is_tail) {
                     const int tail = sg.tail_index + t - sg.first_tail;
                     bar_wait(bTail + 8 * (tail % kRing), (tail / kRing) & 1, ok);
@@ -930,30 +965,30 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         else
                             vs = smem + (sKV - sQ) + (2 * (i0 + t) + 1) % slots * slot_bytes;
                         __syncwarp();
+                        if (quad == 0)
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + c, o);
-                            if (t < dt)
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + c, o);
+                                if (t < dt)
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = 0u;
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = 0u;
 #pragma unroll 1
-                            for (int k = 0; k < 32 * C::NCH; ++k) {
-                                const int kr = quad * 32 * C::NCH + k; // row of the slot
-                                if (!((odd[kr >> 5] >> (kr & 31)) & 1) || !((seen(k >> 5) >> (k & 31)) & 1))
-                                    continue;
+                                for (int k = 0; k < kTile; ++k) {
+                                    if (!((odd[k >> 5] >> (k & 31)) & 1) || !((seen(k >> 5) >> (k & 31)) & 1))
+                                        continue;
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const uint16_t b = *reinterpret_cast<const uint16_t *>(vs + op_off(kr, (c + e) >> 3) + 2 * (e & 7));
-                                    const float x = C::F8 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
-                                    if (!isfinite(x))
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                                    for (int e = 0; e < 16; ++e) {
+                                        const uint16_t b = *reinterpret_cast<const uint16_t *>(vs + op_off(k, (c + e) >> 3) + 2 * (e & 7));
+                                        const float x = C::F8 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
+                                        if (!isfinite(x))
+                                            o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                                    }
                                 }
+                                __syncwarp();
+                                tmem_st16(tO + c, o);
                             }
-                            __syncwarp();
-                            tmem_st16(tO + c, o);
-                        }
                         tmem_st_wait();
                         // every group that reads the slot has read it
                         if constexpr (C::TWO)
@@ -985,93 +1020,106 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
 
             // ---- the segment's end -----------------------------------------------
-            // The sources of a row (its copies, in one group or both) are joined
-            // through shared memory, as many columns at a time as the rows in use
-            // leave room for, and written by consecutive threads, so that the
-            // stores are whole sectors.
+            // A row's lane has its sums; with both groups at it, either writes half
+            // of the columns, after an exchange of the other half between the two
+            // warps that have the row. Sixteen columns of a warp's rows go through
+            // shared memory, so that the stores are whole sectors.
             if (takes) {
-                bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
-                __syncwarp();
-                tc_after();
-                const int nsrc = both ? 2 * C::COPIES : C::COPIES;
-                const int base = both ? 0 : grp * C::COPIES, src = grp * C::COPIES + quad; // first source, this one
-                float4 *buf = reinterpret_cast<float4 *>(smem + (sJoin - sQ));
-                float *part = part_of(p, blockIdx.x, sg.which, MT, D) + (C::TWO ? grp * 128 * D : 0);
-                auto sync = [&] {
-                    if (both)
-                        named_sync<2 * kGroup>(1);
-                    else
-                        named_sync<kGroup>(2 + grp);
-                };
-                s_m[src][row] = m;
-                s_l[src][row] = l;
-                sync();
-                float top = -INFINITY, sum = 0.0f;
-                for (int c = base; c < base + nsrc; ++c)
-                    top = fmaxf(top, s_m[c][row]);
-                for (int c = base; c < base + nsrc; ++c) { // one that saw nothing has l = 0 (or NaN)
-                    const float mc = s_m[c][row], lc = s_l[c][row];
-                    sum += mc == -INFINITY ? lc : lc * exp2_fast(mc - top);
+                if constexpr (C::FEW) {
+                    s_l[grp][quad][row] = l;
+                    named_sync<kGroup>(2 + grp);
                 }
-                float f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
-                if (sg.whole) // the sums' inverse and the values' scale, on the way
-                    f *= sum == 0.0f ? 0.0f : p.cache.v_scale / sum;
-                if (src == base) {
+                if (quad == 0 && warp_live) {
+                    bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
+                    __syncwarp();
+                    tc_after();
+                    if constexpr (C::FEW)
+                        l = (s_l[grp][0][row] + s_l[grp][1][row]) + (s_l[grp][2][row] + s_l[grp][3][row]);
+                    const int pair = 5 + wq; // the barrier of the row's two warps
+                    float top = m, all = l, f = 1.0f;
+                    if (both) {
+                        s_m[grp][0][row] = m;
+                        if constexpr (C::FEW)
+                            __syncwarp();
+                        s_l[grp][0][row] = l;
+                        named_sync<64>(pair);
+                        const float mo = s_m[grp ^ 1][0][row], lo = s_l[grp ^ 1][0][row];
+                        top = fmaxf(m, mo);
+                        // one that saw nothing has l = 0 (or NaN) and O = 0
+                        f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
+                        const float fo = mo == -INFINITY ? 1.0f : exp2_fast(mo - top);
+                        all = l * f + lo * fo;
+                    }
+                    float *part = part_of(p, blockIdx.x, sg.which, MT, D);
                     const long long tk = sg.tok + tok_i;
                     const int hq = sg.h * G + g - ti * G;
-                    s_row[grp][row] = tk * p.ld_out + (long long)hq * D;
-                    if (live && !sg.whole) {
-                        part[(C::TWO ? (256 - grp * 128) * D + grp * 128 : MT * D) + row] = top;
-                        part[(C::TWO ? (256 - grp * 128) * D + 256 + grp * 128 : MT * D + MT) + row] = sum;
-                    } else if (live && p.lse) {
-                        p.lse[tk * p.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    if (live && (!both || grp == 0)) {
+                        if (!sg.whole) {
+                            part[MT * D + trow] = top;
+                            part[MT * D + MT + trow] = all;
+                        } else if (p.lse) {
+                            p.lse[tk * p.Hq + hq] = all == 0.0f ? -INFINITY : (top + log2f(all)) * kLn2;
+                        }
                     }
-                }
-                const int wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
-                const long long *rows = s_row[both ? 0 : grp];
-                // live rows come first
-                const int used = min(C::ROWS, sg.n * G - sg.rt * MT - (C::TWO ? grp * 128 : 0));
-                int lg = 2; // 2^lg float4 a row and pass
-                while (lg < (D == 128 ? 5 : 4) && used * (C::COPIES << (lg + 1)) * 16 <= C::JOIN / 2)
-                    ++lg;
-                const int per_row = 1 << lg, mask = min(per_row, 8) - 1;
-                buf += base * (C::JOIN / 2 / 16 / C::COPIES);
-                const int stride = used << lg; // float4 of a source
-                auto place = [&](int rr, int e) { return (rr << lg) + (e ^ ((lg == 2 ? rr >> 1 : rr) & mask)); };
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 4 * per_row) {
-                    if (warp_live)
-#pragma unroll 1
-                        for (int c = 0; c < per_row; c += 4) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + c0 + 4 * c, o);
-                            if (live)
+                    if (sg.whole) // the sum's inverse and the values' scale, on the way
+                        f *= all == 0.0f ? 0.0f : p.cache.v_scale / all;
+                    const long long orow = tk * p.ld_out + (long long)hq * D;
+                    const int row0 = trow - lane; // of this warp, in the tile
+                    const int items = 4 * min(32, sg.n * G - sg.rt * MT - row0); // 16-byte pieces of 16 columns
+                    float4 *mine = reinterpret_cast<float4 *>(smem + (sOut - sQ) + (C::FEW ? grp : warp) * C::OUT1);
+                    const float4 *other = reinterpret_cast<const float4 *>(smem + (sOut - sQ) + (C::FEW ? grp ^ 1 : warp ^ 4) * C::OUT1);
+                    auto place = [](int r, int e) { return r * 4 + (e ^ ((r >> 1) & 3)); };
+                    auto write = [&](const float4 *x, int col) { // 16 columns of this lane's row
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    buf[(src - base) * stride + place(row, c + e)] =
-                                        make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                                    __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
-                            __syncwarp();
-                        }
-                    sync();
-#pragma unroll 1
-                    for (int w = wtid; w < used << lg; w += wth) {
-                        const int rr = w >> lg, e = w & (per_row - 1);
-                        const float4 *b = buf + place(rr, e);
-                        float4 x = b[0];
+                        for (int e = 0; e < 4; ++e)
+                            mine[place(lane, e)] = x[e];
+                        __syncwarp();
 #pragma unroll 4
-                        for (int c = 1; c < nsrc; ++c) {
-                            const float4 y = b[c * stride];
-                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        for (int k = lane; k < ((items + 31) & ~31); k += 32) {
+                            const int r = k >> 2, e = k & 3;
+                            const long long at = __shfl_sync(~0u, orow, r);
+                            if (k < items) {
+                                const float4 y = mine[place(r, e)];
+                                if (sg.whole)
+                                    *reinterpret_cast<uint2 *>(p.out + at + col + 4 * e) = make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
+                                else
+                                    *reinterpret_cast<float4 *>(part + (size_t)(row0 + r) * D + col + 4 * e) = y;
+                            }
                         }
-                        if (sg.whole)
-                            *reinterpret_cast<uint2 *>(p.out + rows[rr] + c0 + 4 * e) = make_uint2(pack2<false>(x.x, x.y), pack2<false>(x.z, x.w));
-                        else
-                            *reinterpret_cast<float4 *>(part + (size_t)rr * D + c0 + 4 * e) = x;
+                        __syncwarp();
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t raw[32];
+                        tmem_ld32(tO + c, raw);
+                        tmem_ld_wait(raw);
+                        float4 x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = make_float4(__uint_as_float(raw[4 * e]) * f, __uint_as_float(raw[4 * e + 1]) * f,
+                                               __uint_as_float(raw[4 * e + 2]) * f, __uint_as_float(raw[4 * e + 3]) * f);
+                        if (both) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mine[place(lane, e)] = grp ? x[e] : x[4 + e];
+                            named_sync<64>(pair);
+                            float4 y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 a = grp ? x[4 + e] : x[e], b = other[place(lane, e)];
+                                y[e] = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+                            }
+                            named_sync<64>(pair);
+                            write(y, c + 16 * grp);
+                        } else {
+                            write(x, c);
+                            write(x + 4, c + 16);
+                        }
                     }
-                    sync();
+                    tc_before();
                 }
-                tc_before();
+                if constexpr (C::FEW) // s_l is free again
+                    named_sync<kGroup>(2 + grp);
             }
             __syncwarp();
             if (lane == 0)
@@ -1238,7 +1286,7 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
     while (box < 64 && p.cache.page % (2 * box) == 0)
         box *= 2;
     CUtensorMap kmap{}, vmap{};
-    if (box * std::min(C::ROWB, 128) < kBoxBytes)
+    if (box * std::min(C::ROWB, 128) < kBoxBytes || kTile / box * C::ROWB > 32 * 128) // a lane a piece
         box = 0;
     else if (!encoder())
         return cudaErrorNotSupported;
@@ -1250,11 +1298,11 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
     return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);
 }
 
-// Rows of a tile: what a request has on average, at least 32.
+// Rows of a tile, for what a request has on average.
 int row_tile(int T, int R, int Hq, int Hkv)
 {
     const long long rows = (long long)((T + R - 1) / R) * (Hq / Hkv);
-    return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    return rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
 template <int D, int KV>
@@ -1263,7 +1311,6 @@ cudaError_t launch_d(const AttnProblem &p, int num_sms, cudaStream_t stream)
     const int grid = std::min(num_sms, kMaxGrid);
     switch (row_tile(p.T, p.R, p.Hq, p.cache.heads)) {
     case 32: return launch_t<D, KV, 32>(p, grid, stream);
-    case 64: return launch_t<D, KV, 64>(p, grid, stream);
     case 128: return launch_t<D, KV, 128>(p, grid, stream);
     default: return launch_t<D, KV, 256>(p, grid, stream);
     }
