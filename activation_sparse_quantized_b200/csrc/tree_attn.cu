@@ -89,7 +89,7 @@ struct Cfg {
     static constexpr int SLOTS = F8 ? KV_BYTES / (kTile * D) : KV_BYTES / SLOT;
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
     static constexpr int ROWB = F8 ? D : 2 * D, CPR = ROWB / 16; // bytes, 16-byte chunks of a key
-    static constexpr int OUT1 = 32 * 64, OUT = (FEW ? 2 : 8) * OUT1; // a writing warp's 32 rows x 16 columns
+    static constexpr int OUT1 = 32 * 64, OUT = MT == 128 ? 8 * OUT1 : 0; // 16 columns of a warp's rows, for the other group
     static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 2;
     static constexpr int SMEM = 1024 + Q + P + KV_BYTES + NV * SLOT + OUT + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ Seg s_seg[kRing];
     __shared__ float s_m[2][C::COPIES][C::ROWS], s_l[2][C::COPIES][C::ROWS]; // by group and copy
     __shared__ float s_mx[C::FEW ? 4 : 1][C::COPIES][C::FEW ? 32 : 1];       // a tile's maxima, by group and turn
+    __shared__ long long s_out[C::FEW ? 2 : 1][C::FEW ? 32 : 1];             // where rows are written
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
     __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
     __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
@@ -1020,74 +1021,123 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
 
             // ---- the segment's end -----------------------------------------------
-            // A row's lane has its sums; with both groups at it, either writes half
-            // of the columns, after an exchange of the other half between the two
-            // warps that have the row. Sixteen columns of a warp's rows go through
-            // shared memory, so that the stores are whole sectors.
-            if (takes) {
-                if constexpr (C::FEW) {
-                    s_l[grp][quad][row] = l;
-                    named_sync<kGroup>(2 + grp);
-                }
-                if (quad == 0 && warp_live) {
-                    bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
-                    __syncwarp();
-                    tc_after();
-                    if constexpr (C::FEW)
-                        l = (s_l[grp][0][row] + s_l[grp][1][row]) + (s_l[grp][2][row] + s_l[grp][3][row]);
-                    const int pair = 5 + wq; // the barrier of the row's two warps
-                    float top = m, all = l, f = 1.0f;
+            if (takes && warp_live) {
+                float *part = part_of(p, blockIdx.x, sg.which, MT, D);
+                const long long tk = sg.tok + tok_i;
+                const int hq = sg.h * G + g - ti * G;
+                const long long orow = tk * p.ld_out + (long long)hq * D;
+                // A group's reference and sum (m, l), joined with the other's where
+                // both have keys: l becomes the row's sum, the result the factor of
+                // this group's O. One that saw nothing has l = 0 (or NaN) and O = 0.
+                auto join = [&](float mo, float lo) {
+                    const float top = both ? fmaxf(m, mo) : m;
+                    float f = 1.0f;
                     if (both) {
-                        s_m[grp][0][row] = m;
-                        if constexpr (C::FEW)
-                            __syncwarp();
-                        s_l[grp][0][row] = l;
-                        named_sync<64>(pair);
-                        const float mo = s_m[grp ^ 1][0][row], lo = s_l[grp ^ 1][0][row];
-                        top = fmaxf(m, mo);
-                        // one that saw nothing has l = 0 (or NaN) and O = 0
                         f = m == -INFINITY ? 1.0f : exp2_fast(m - top);
                         const float fo = mo == -INFINITY ? 1.0f : exp2_fast(mo - top);
-                        all = l * f + lo * fo;
+                        l = l * f + lo * fo;
                     }
-                    float *part = part_of(p, blockIdx.x, sg.which, MT, D);
-                    const long long tk = sg.tok + tok_i;
-                    const int hq = sg.h * G + g - ti * G;
-                    if (live && (!both || grp == 0)) {
+                    if (live && quad == 0 && (!both || grp == 0)) {
                         if (!sg.whole) {
                             part[MT * D + trow] = top;
-                            part[MT * D + MT + trow] = all;
+                            part[MT * D + MT + trow] = l;
                         } else if (p.lse) {
-                            p.lse[tk * p.Hq + hq] = all == 0.0f ? -INFINITY : (top + log2f(all)) * kLn2;
+                            p.lse[tk * p.Hq + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
                         }
                     }
                     if (sg.whole) // the sum's inverse and the values' scale, on the way
-                        f *= all == 0.0f ? 0.0f : p.cache.v_scale / all;
-                    const long long orow = tk * p.ld_out + (long long)hq * D;
-                    const int row0 = trow - lane; // of this warp, in the tile
-                    const int items = 4 * min(32, sg.n * G - sg.rt * MT - row0); // 16-byte pieces of 16 columns
-                    float4 *mine = reinterpret_cast<float4 *>(smem + (sOut - sQ) + (C::FEW ? grp : warp) * C::OUT1);
-                    const float4 *other = reinterpret_cast<const float4 *>(smem + (sOut - sQ) + (C::FEW ? grp ^ 1 : warp ^ 4) * C::OUT1);
-                    auto place = [](int r, int e) { return r * 4 + (e ^ ((r >> 1) & 3)); };
-                    auto write = [&](const float4 *x, int col) { // 16 columns of this lane's row
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mine[place(lane, e)] = x[e];
-                        __syncwarp();
-#pragma unroll 4
-                        for (int k = lane; k < ((items + 31) & ~31); k += 32) {
-                            const int r = k >> 2, e = k & 3;
-                            const long long at = __shfl_sync(~0u, orow, r);
-                            if (k < items) {
-                                const float4 y = mine[place(r, e)];
-                                if (sg.whole)
-                                    *reinterpret_cast<uint2 *>(p.out + at + col + 4 * e) = make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
-                                else
-                                    *reinterpret_cast<float4 *>(part + (size_t)(row0 + r) * D + col + 4 * e) = y;
-                            }
-                        }
-                        __syncwarp();
+                        f *= l == 0.0f ? 0.0f : p.cache.v_scale / l;
+                    return f;
+                };
+                if constexpr (C::FEW) {
+                    // The first warp of a group has all of its O. Half of the columns
+                    // at a time go where P was, and all the warps write them out.
+                    auto sync = [&] {
+                        if (both)
+                            named_sync<2 * kGroup>(1);
+                        else
+                            named_sync<kGroup>(2 + grp);
                     };
+                    s_l[grp][quad][row] = l;
+                    if (quad == 0) {
+                        s_m[grp][0][row] = m;
+                        s_out[grp][row] = orow;
+                    }
+                    bar_wait(bO + 8 * grp, s_ph ^ 1, ok); // this group's O is complete
+                    __syncwarp();
+                    tc_after();
+                    sync();
+                    l = (s_l[grp][0][row] + s_l[grp][1][row]) + (s_l[grp][2][row] + s_l[grp][3][row]);
+                    const int og = grp ^ 1;
+                    const float f = join(s_m[og][0][row], (s_l[og][0][row] + s_l[og][1][row]) + (s_l[og][2][row] + s_l[og][3][row]));
+                    float4 *out = reinterpret_cast<float4 *>(smem + (sP - sQ));
+                    const int wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
+                    const int used = min(32, sg.n * G - sg.rt * MT);
+                    const float4 *a = out + (both ? 0 : grp) * (C::P1 / 16);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        if (quad == 0)
+#pragma unroll
+                            for (int c = 0; c < 64; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + c0 + c, o);
+                                tmem_ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    out[grp * (C::P1 / 16) + row * 16 + ((c / 4 + e) ^ (row & 7))] =
+                                        make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                    __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                            }
+                        sync();
+                        // rows next to each other in a part, columns in the output
+#pragma unroll 2
+                        for (int k = wtid; k < 512; k += wth) {
+                            const int r = sg.whole ? k >> 4 : k & 31, e = sg.whole ? k & 15 : k >> 5;
+                            if (r >= used)
+                                continue;
+                            const int at = r * 16 + (e ^ (r & 7));
+                            float4 x = a[at];
+                            if (both) {
+                                const float4 y = a[C::P1 / 16 + at];
+                                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                            }
+                            if (sg.whole)
+                                *reinterpret_cast<uint2 *>(p.out + s_out[both ? 0 : grp][r] + c0 + 4 * e) = make_uint2(pack2<false>(x.x, x.y), pack2<false>(x.z, x.w));
+                            else
+                                reinterpret_cast<float4 *>(part)[(c0 / 4 + e) * MT + r] = x;
+                        }
+                        sync();
+                    }
+                } else {
+                    bar_wait(bO + 8 * grp, s_ph ^ 1, ok);
+                    __syncwarp();
+                    tc_after();
+                    const int pair = 5 + wq; // the barrier of the row's two warps
+                    if (both) {
+                        s_m[grp][0][row] = m;
+                        s_l[grp][0][row] = l;
+                        named_sync<64>(pair);
+                    }
+                    const float f = join(s_m[grp ^ 1][0][row], s_l[grp ^ 1][0][row]);
+                    // Sixteen columns of a row: rows next to each other in a part,
+                    // whole sectors of the output.
+                    auto write = [&](const float4 *x, int col) {
+                        if (live && sg.whole) {
+                            uint4 *o = reinterpret_cast<uint4 *>(p.out + orow + col);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                o[e] = make_uint4(pack2<false>(x[2 * e].x, x[2 * e].y), pack2<false>(x[2 * e].z, x[2 * e].w),
+                                                  pack2<false>(x[2 * e + 1].x, x[2 * e + 1].y), pack2<false>(x[2 * e + 1].z, x[2 * e + 1].w));
+                        } else if (live) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                reinterpret_cast<float4 *>(part)[(col / 4 + e) * MT + trow] = x[e];
+                        }
+                    };
+                    // with both groups at it, either writes half of the columns, after
+                    // an exchange of the other half between the row's two warps
+                    float4 *mine = reinterpret_cast<float4 *>(smem + (sOut - sQ) + warp * C::OUT1);
+                    const float4 *other = reinterpret_cast<const float4 *>(smem + (sOut - sQ) + (warp ^ 4) * C::OUT1);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t raw[32];
@@ -1101,25 +1151,25 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         if (both) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                mine[place(lane, e)] = grp ? x[e] : x[4 + e];
+                                mine[lane * 4 + (e ^ ((lane >> 1) & 3))] = grp ? x[e] : x[4 + e];
                             named_sync<64>(pair);
-                            float4 y[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float4 a = grp ? x[4 + e] : x[e], b = other[place(lane, e)];
-                                y[e] = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+                                const float4 b = other[lane * 4 + (e ^ ((lane >> 1) & 3))];
+                                if (grp)
+                                    x[e] = x[4 + e];
+                                x[e] = make_float4(x[e].x + b.x, x[e].y + b.y, x[e].z + b.z, x[e].w + b.w);
                             }
                             named_sync<64>(pair);
-                            write(y, c + 16 * grp);
+                            write(x, c + 16 * grp);
                         } else {
                             write(x, c);
                             write(x + 4, c + 16);
                         }
+                        __syncwarp();
                     }
-                    tc_before();
                 }
-                if constexpr (C::FEW) // s_l is free again
-                    named_sync<kGroup>(2 + grp);
+                tc_before();
             }
             __syncwarp();
             if (lane == 0)
@@ -1137,47 +1187,48 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-// Joins the parts of the items that several CTAs worked on, in key order. The
-// CTAs of an item share its rows here too: CTA c0 + x takes rows x, x + parts,
-// ... A row is read by as many of the CTA's warps as there are rows too few.
+// Joins the parts of the items that several CTAs worked on, in key order. A unit
+// is 8 rows of 16 columns (a lane: one row, four columns); the CTAs of an item
+// share its units, CTA c0 + x taking units x, x + parts, ..., and a CTA's warps
+// share the parts of each where there are fewer units than warps.
 constexpr int kJoinWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem p, int MT)
 {
-    constexpr int LPR = D / 4;     // lanes per row: with D = 64 two parts are read side by side
-    constexpr int SIDE = 32 / LPR, BATCH = 4;
-    __shared__ float4 s_o[kJoinWarps][LPR];
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = lane % LPR;
+    constexpr int BATCH = 4;
+    __shared__ float4 s_o[kJoinWarps][32];
+    __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_launch_dependents();
     grid_dependency_wait();
     const Split sp = static_cast<const Split *>(p.workspace)[blockIdx.x];
     if (sp.parts == 0)
         return;
     const int G = p.Hq / p.cache.heads, first = (int)(blockIdx.x >> 1) - sp.c0;
-    const int rows = min((long long)MT, (long long)sp.n * G - (long long)sp.rt * MT);
-    const int mine = rows > first ? (rows - first + sp.parts - 1) / sp.parts : 0;
-    int wpr = kJoinWarps; // warps per row
-    while (wpr > 1 && wpr * mine > kJoinWarps)
-        wpr >>= 1;
-    for (int k0 = 0; k0 < mine; k0 += kJoinWarps / wpr) {
-        const int k = k0 + warp / wpr, row = first + k * sp.parts;
+    const int rows = (int)min((long long)MT, (long long)sp.n * G - (long long)sp.rt * MT);
+    const int units = (rows + 7) / 8 * (D / 16);
+    const int mine = units > first ? (units - first + sp.parts - 1) / sp.parts : 0;
+    int wpu = kJoinWarps; // warps per unit
+    while (wpu > 1 && wpu * mine > kJoinWarps)
+        wpu >>= 1;
+    for (int k0 = 0; k0 < mine; k0 += kJoinWarps / wpu) {
+        const int k = k0 + warp / wpu, u = first + k * sp.parts;
+        const int row = u / (D / 16) * 8 + (lane & 7), c4 = u % (D / 16) * 4 + (lane >> 3);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = -INFINITY, l = 0.0f;
-        if (k < mine) {
-            const int step = SIDE * wpr;
-            for (int b = (warp % wpr) * SIDE + lane / LPR; b < sp.parts; b += BATCH * step) {
+        if (k < mine && row < rows) {
+            for (int b = warp % wpu; b < sp.parts; b += BATCH * wpu) {
                 float pm[BATCH], pl[BATCH];
                 float4 v[BATCH];
 #pragma unroll
                 for (int e = 0; e < BATCH; ++e) {
-                    const int c = b + e * step;
-                    const float *part = part_of(p, sp.c0 + c, c == 0, MT, D);
+                    const int c = b + e * wpu;
                     const bool in = c < sp.parts;
+                    const float *part = part_of(p, sp.c0 + (in ? c : 0), !in || c == 0, MT, D);
                     pm[e] = in ? part[MT * D + row] : -INFINITY;
                     pl[e] = in ? part[MT * D + MT + row] : 0.0f;
-                    v[e] = in ? *reinterpret_cast<const float4 *>(part + (size_t)row * D + 4 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[e] = in ? reinterpret_cast<const float4 *>(part)[c4 * MT + row] : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 float top = m;
 #pragma unroll
@@ -1195,43 +1246,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
                 }
             }
         }
-        if constexpr (SIDE == 2) {
-            const float m2 = __shfl_xor_sync(~0u, m, 16), l2 = __shfl_xor_sync(~0u, l, 16);
-            const float4 v = make_float4(__shfl_xor_sync(~0u, o.x, 16), __shfl_xor_sync(~0u, o.y, 16),
-                                         __shfl_xor_sync(~0u, o.z, 16), __shfl_xor_sync(~0u, o.w, 16));
-            const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
-            const float f = exp2_fast(m - ref), w = exp2_fast(m2 - ref);
-            o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
-            l = l * f + l2 * w;
-            m = top;
-        }
-        if (wpr > 1) {
-            if (lane < LPR)
-                s_o[warp][x] = o;
-            if (lane == 0) {
-                s_m[warp] = m;
-                s_l[warp] = l;
-            }
+        if (wpu > 1) {
+            s_o[warp][lane] = o;
+            s_m[warp][lane] = m;
+            s_l[warp][lane] = l;
             __syncthreads();
-            if (warp % wpr == 0) {
-                for (int w = warp + 1; w < warp + wpr; ++w) {
-                    const float m2 = s_m[w], top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
-                    const float f = exp2_fast(m - ref), e = exp2_fast(m2 - ref);
-                    const float4 v = s_o[w][x];
-                    o = make_float4(o.x * f + v.x * e, o.y * f + v.y * e, o.z * f + v.z * e, o.w * f + v.w * e);
-                    l = l * f + s_l[w] * e;
-                    m = top;
+            if (warp % wpu == 0) {
+                float top = m;
+                for (int w = 1; w < wpu; ++w)
+                    top = fmaxf(top, s_m[warp + w][lane]);
+                const float ref = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - ref);
+                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                l *= f;
+                m = top;
+#pragma unroll 4
+                for (int w = 1; w < wpu; ++w) {
+                    const float e = exp2_fast(s_m[warp + w][lane] - ref);
+                    const float4 v = s_o[warp + w][lane];
+                    o = make_float4(o.x + v.x * e, o.y + v.y * e, o.z + v.z * e, o.w + v.w * e);
+                    l += s_l[warp + w][lane] * e;
                 }
             }
             __syncthreads();
         }
-        if (k < mine && warp % wpr == 0 && lane < LPR) {
+        if (k < mine && row < rows && warp % wpu == 0) {
             const int g = sp.rt * MT + row, ti = g / G, hq = sp.h * G + g - ti * G;
             const long long t = sp.tok + ti;
             const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
-            *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + 4 * x) =
+            *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + 4 * c4) =
                 make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
-            if (p.lse && x == 0)
+            if (p.lse && c4 == 0)
                 p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
     }

@@ -61,7 +61,8 @@ struct __align__(32) Split {
     int parts, c0, tok, n, h, rt;
 };
 
-// The part that CTA c leaves of either: MT rows of D sums, then the rows'
+// The part that CTA c leaves of either: D sums of MT rows, four of a row side by
+// side and the rows next to each other ([D / 4][MT][4]), then the rows'
 // references, then their sums.
 __device__ __forceinline__ float *part_of(const AttnProblem &p, int c, int which, int MT, int D)
 {
