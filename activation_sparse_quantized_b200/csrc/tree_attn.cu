@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             bar_init(bSeg + 8 * b, 1);
             bar_init(bSegFree + 8 * b, kSoftWarps);
         }
-        bar_init(bQ, C::QW);
+        bar_init(bQ, C::F8 || C::FEW ? C::QW : 32 * C::QW);
         bar_init(bQFree, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     if (lane == 0)
                         bar_expect(full, kTile * C::ROWB);
                     __syncwarp();
-#pragma unroll 4
+#pragma unroll 8
                     for (int x = 0; x < pieces; ++x) {
                         const int at = __shfl_sync(~0u, pid, x), s = __shfl_sync(~0u, slot, x);
                         tma_load_4d(dst + x % PARTS * C::SUB + x / PARTS * box * min(C::ROWB, 128), map, x % PARTS * 64, s, h, at,
@@ -618,12 +618,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         // row is scaled by the power of two that brings its largest value into
         // [2^7, 2^8) and split in two 8-bit parts, 4 bits each of its 8: exact
         // for values down to 2^-2, below it off by at most 2^-10, i.e. 2^-17 of
-        // the largest. A negative scale's sign goes to q, so that the largest
-        // score is the largest exponent.
+        // the largest.
         constexpr int QT = 32 * C::QW, CH = D / 8;           // 16-byte chunks of a row
         constexpr int ALL = (C::TWO ? 256 : MT) * CH / QT, N = ALL < 16 ? ALL : 16;
         const int ct = tid - 32 * kQ;
-        const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
         const uint32_t inv_g = 0xffffffffu / (uint32_t)G + 1; // x / G = (x inv_g) >> 32 for x G < 2^32
         Ring seg{0, 0};
         uint32_t free_ph = 1; // the operand is free at first
@@ -636,6 +634,21 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             const int tok = s_seg[seg.s].tok, n = s_seg[seg.s].n, h = s_seg[seg.s].h, g0 = s_seg[seg.s].rt * MT;
             seg.step(1, kRing);
             const int t0 = g0 / G, rem0 = g0 - t0 * G;
+            if constexpr (!C::F8 && !C::FEW) {
+                // many rows: straight into their places
+                bar_wait(bQFree, free_ph, ok);
+                __syncwarp();
+#pragma unroll 4
+                for (int k = 0; k < ALL; ++k) {
+                    const int idx = ct + k * QT, qr = idx / CH, x = rem0 + qr;
+                    const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
+                    const uint16_t *src = p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D + 8 * (idx % CH);
+                    cp_async16_zfill(sQ + (qr >> 7) * C::Q1 + op_off(qr & 127, idx % CH), ti < n ? src : p.q, ti < n);
+                }
+                cp_async_arrive(bQ);
+                free_ph ^= 1;
+                continue;
+            }
 #pragma unroll 1
             for (int k0 = 0; k0 < ALL; k0 += N) {
                 uint4 v[N];
@@ -656,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     const int idx = ct + (k0 + k) * QT, qr = idx / CH, c = idx % CH;
                     uint8_t *dst = smem + (C::TWO ? (qr >> 7) * C::Q1 : 0);
                     const int r = C::TWO ? qr & 127 : qr;
-                    const uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
+                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                     if constexpr (C::F8) {
                         float f[8], mx = 0.0f;
 #pragma unroll
@@ -861,6 +874,14 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     for (int e = 0; e < 32; ++e)
                         s[e] = (vis >> e) & 1 ? s[e] : 0xff800000u;
                 };
+                // A negative scale's sign goes to the scores, so that the largest
+                // one is the largest exponent.
+                auto turn = [&](uint32_t *s) {
+                    if (p.scale < 0.0f)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[e] ^= 0x80000000u;
+                };
                 auto highest = [](const uint32_t *s, float *mx) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -907,6 +928,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     uint32_t s[32], w[16];
                     tmem_ld32(tS + 32 * quad, s);
                     tmem_ld_wait(s);
+                    turn(s);
                     if (masked)
                         mask(s, quad);
                     highest(s, mx);
@@ -925,20 +947,20 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                             make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                     fence_async_smem();
                 } else if (warp_live) {
-                    // twice over the scores; masked ones go back for the second time
+                    // twice over the scores; changed ones go back for the second time
                     uint32_t s[32];
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(tS + 32 * c, s);
                         tmem_ld_wait(s);
-                        if (masked) {
+                        turn(s);
+                        if (masked)
                             mask(s, c);
+                        if (masked || p.scale < 0.0f)
                             tmem_st32(tS + 32 * c, s);
-                        }
                         highest(s, mx);
                     }
-                    if (masked)
-                        tmem_st_wait();
+                    tmem_st_wait();
                     const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {

@@ -432,6 +432,11 @@ def test_attention_counts_out_of_range_are_clamped_and_flagged():
 def test_attention_peaked_and_extreme_scores():
     AttnCase([500], [4], 8, 2, 128, 16, "nhd", BF16, None, seed=1, q_scale=40.0).run().check()
     AttnCase([500], [4], 8, 2, 128, 16, "nhd", E4M3, None, seed=1, q_scale=40.0).run().check()
+    for Hq, n, dtype in ((4, 2, BF16), (4, 2, E4M3), (8, 9, BF16), (8, 40, BF16), (8, 9, E4M3)):   # negative and zero scales
+        for scale in (-0.3, 0.0):
+            c = AttnCase([300], [n], Hq, 1, 64, 16, "nhd", dtype, "random", seed=n)
+            c.scale = scale
+            c.run().check()
     for big in (1e30, 1e-30):       # q far outside fp16, scale bringing the scores back
         c = AttnCase([130], [2], 4, 1, 64, 16, "nhd", E4M3, None, seed=1)
         c.q = (c.q.float() * big).to(BF16)
