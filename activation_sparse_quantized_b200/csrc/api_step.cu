@@ -124,8 +124,6 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
         (q && (!stride_ok(ld_q, Hq * D, 2) || !stride_ok(ld_qo, Hq * D, 2))) ||
         (rope && rope_len < 1))
         return SGQ_ERR_SHAPE;
-    if ((long long)T * ((q ? Hq : 0) + 2 * Hkv) * (D / 16) > (1ll << 38))
-        return SGQ_ERR_SHAPE;
     const int sms = sgq::current_device_sms();
     if (sms < 0)
         return sms;

@@ -13,7 +13,7 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // The plan: whole-number prefix sums over the requests, then one output row
-// per new token.
+// per new token and one table entry per new page.
 //
 //   cu[r]   = min(max_tokens, sum over s < r of n_s)
 //   want_r  = ceil((l_r + n_r) / page),  need_r = max(0, want_r - held_r)
@@ -22,12 +22,20 @@ namespace {
 //   number base_r + (j - held_r) from its end
 //
 // One cluster of up to 8 CTAs: every CTA makes the sums for itself (the inputs
-// are a few KB), then the CTAs share out the tokens and the table rows. The
-// cluster's barrier stands between the last read of held and free_count and
-// the first write of held_out and free_count_out, which may be the same words.
+// are a few KB), then the CTAs share out the pages and the tokens, each found
+// by bisection of its prefix sum, so that one long request is shared as well as
+// many short ones. The cluster's barrier stands between the last read of held
+// and free_count and the first write of held_out and free_count_out, which may
+// be the same words. What bounds it is latency: a load, two scans, a load.
+//
+// More tokens than the cluster has threads go to a second kernel over all SMs,
+// which reads the slots off the finished table: 16 requests with 136 tokens
+// take 4.4 us on the one kernel, and 2000 requests with 301,000 tokens 10 us on
+// two, 75 us on one.
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -80,20 +88,80 @@ __device__ __forceinline__ long long block_scan(long long v, long long *part, lo
     return s - v + (warp ? before : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanProblem p)
+// The largest v of the CTA's threads, in each of them. Not before the threads
+// are done with part.
+__device__ __forceinline__ long long block_max(long long v, long long *part)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = max(v, __shfl_xor_sync(~0u, v, o));
+    if (lane == 0)
+        part[warp] = v;
+    __syncthreads();
+    v = part[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = max(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+// The last r < R with sum[r] <= x; sum is non-decreasing from 0.
+__device__ __forceinline__ int place_in(const int32_t *sum, int R, int x)
+{
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sum[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Pages of len + n tokens (both at most 2^30).
+__device__ __forceinline__ int pages_of(int len, int n, int page)
+{
+    return (int)(((uint32_t)len + n + page - 1) / (uint32_t)page);
+}
+
+// Row t of the outputs: new token i of request r, on page `id` (-1: none).
+__device__ __forceinline__ int put_token(const PlanProblem &p, int t, int r, int i, int len, int id, int off, bool served)
+{
+    int bits = 0;
+    long long slot = -1;
+    if (served) {
+        if (id >= 0 && id < p.num_pages)
+            slot = (long long)id * p.page + off;
+        else
+            bits = SGQ_STATUS_BAD_INDEX;
+    }
+    p.slots[t] = slot;
+    if (p.pos)
+        p.pos[t] = len + (p.depth ? p.depth[t] : i);
+    if (p.req)
+        p.req[t] = r;
+    return bits;
+}
+
+// rows: whether this kernel writes the tokens' rows (else token_kernel does).
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanProblem p, const int rows)
 {
     extern __shared__ int32_t sh[];
     __shared__ long long part[32];
-    int32_t *cu = sh;            // [R + 1]
-    int32_t *base = cu + p.R + 1; // [R] first free-list entry, or -1: not served
-    int32_t *len = base + p.R;   // [R]
-    int32_t *held = len + p.R;   // [R]
+    int32_t *cu = sh;               // [R + 1]
+    int32_t *base = cu + p.R + 1;   // [R], sums of pages, up to INT_MAX
+    int32_t *len = base + p.R;      // [R]
+    int32_t *held = len + p.R;      // [R]
     const int tid = threadIdx.x;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int gtid = (int)rank * kPlanThreads + tid, gsize = (int)ctas * kPlanThreads;
     int bits = 0;
     grid_launch_dependents();
     grid_dependency_wait();
 
+    const int count = *p.free_count;
     for (int r = tid; r < p.R; r += kPlanThreads) {
         int l = p.lens[r], n = p.news[r], h = p.held[r];
         // a request whose state cannot be is given no tokens
@@ -107,8 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanProblem p)
         base[r] = n;
         held[r] = h;
     }
-    const long long avail = min(max(*p.free_count, 0), p.num_pages);
-    if (*p.free_count != avail)
+    const int avail = min(max(count, 0), p.num_pages);
+    if (count != avail)
         bits |= SGQ_STATUS_BAD_COUNT;
     __syncthreads();
     if (ctas > 1)
@@ -131,108 +199,101 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanProblem p)
         cu[p.R] = (int32_t)min(total, (long long)p.max_tokens);
     __syncthreads();
 
-    // pages
-    sum = 0;
-    for (int r = r0; r < r1; ++r) {
+    // pages: needed ones, -1 for a request longer than a table row
+    auto need_of = [&](int r) {
         const int n = cu[r + 1] - cu[r];
-        const long long want = n ? ((long long)len[r] + n + p.page - 1) / p.page : 0;
-        int need = (int)max(0ll, min(want, (long long)p.table_ld + 1) - held[r]);
-        if (want > p.table_ld) { // longer than a table row
-            bits |= SGQ_STATUS_BAD_COUNT;
-            need = -1;
-        }
-        base[r] = need;
-        sum += max(need, 0);
-    }
+        const int want = n ? pages_of(len[r], n, p.page) : 0;
+        return want > p.table_ld ? -1 : max(0, want - held[r]);
+    };
+    sum = 0;
+    for (int r = r0; r < r1; ++r)
+        sum += max(need_of(r), 0);
     at = block_scan(sum, part, total);
+    // the pages of the requests before the first that does not fit
+    long long used = total;
     for (int r = r0; r < r1; ++r) {
-        const int need = base[r];
-        const bool served = need == 0 || (need > 0 && at + need <= avail);
-        if (need > 0 && !served)
-            bits |= SGQ_STATUS_NO_PAGES;
-        base[r] = served ? (int32_t)min(at, avail) : -1;
+        const int need = need_of(r);
+        if (need < 0)
+            bits |= SGQ_STATUS_BAD_COUNT;
+        base[r] = (int32_t)min(at, 0x7fffffffll);
         at += max(need, 0);
+        if (need > 0 && at > avail) {
+            bits |= SGQ_STATUS_NO_PAGES;
+            used = min(used, at - need);
+        }
+    }
+    if (total > avail) {
+        __syncthreads();
+        used = -block_max(-used, part);
     }
     __syncthreads();
+    auto served = [&](int r, int need) { return need == 0 || (need > 0 && (long long)base[r] + need <= avail); };
+    auto fresh = [&](int r, int j) { return p.free_pages[avail - 1 - (base[r] + (j - held[r]))]; };
 
     // new tokens
-    const int T = cu[p.R];
-    for (int t = rank * kPlanThreads + tid; t < T; t += ctas * kPlanThreads) {
-        int lo = 0, hi = p.R; // cu[lo] <= t < cu[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int i = t - cu[lo];
-        long long slot = -1;
-        if (base[lo] >= 0) {
-            const long long at_pos = (long long)len[lo] + i;
-            const int j = (int)(at_pos / p.page), off = (int)(at_pos - (long long)j * p.page);
-            const int id = j < held[lo]
-                               ? p.table[(long long)lo * p.table_ld + j]
-                               : p.free_pages[avail - 1 - (base[lo] + (j - held[lo]))];
-            if (id >= 0 && id < p.num_pages)
-                slot = (long long)id * p.page + off;
-            else
-                bits |= SGQ_STATUS_BAD_INDEX;
-        }
-        p.slots[t] = slot;
-        if (p.pos)
-            p.pos[t] = len[lo] + (p.depth ? p.depth[t] : i);
-        if (p.req)
-            p.req[t] = lo;
+    const int T = rows ? cu[p.R] : 0;
+    for (int t = gtid; t < T; t += gsize) {
+        const int r = place_in(cu, p.R, t), i = t - cu[r];
+        const uint32_t at_pos = (uint32_t)len[r] + i; // below 2^31
+        const bool ok = served(r, need_of(r));
+        const int j = at_pos / (uint32_t)p.page, off = at_pos - j * p.page;
+        const int id = !ok ? -1 : j < held[r] ? p.table[(long long)r * p.table_ld + j] : fresh(r, j);
+        bits |= put_token(p, t, r, i, len[r], id, off, ok);
     }
 
     if (ctas > 1)
         cluster_wait(); // every CTA has read held and free_count
-    // table rows: one warp per request
-    const int lane = tid & 31;
-    for (int r = rank * (kPlanThreads / 32) + (tid >> 5); r < p.R;
-         r += ctas * (kPlanThreads / 32)) {
-        const int n = cu[r + 1] - cu[r], h = held[r];
-        int want = h;
-        if (n && base[r] >= 0) {
-            want = max(h, (int)(((long long)len[r] + n + p.page - 1) / p.page));
-            for (int j = h + lane; j < want; j += 32)
-                p.table[(long long)r * p.table_ld + j] =
-                    p.free_pages[avail - 1 - (base[r] + (j - h))];
-        }
-        if (lane == 0)
-            p.held_out[r] = want;
+    // new pages
+    for (int q = gtid; q < (int)used; q += gsize) {
+        const int r = place_in(base, p.R, q), j = held[r] + (q - base[r]);
+        p.table[(long long)r * p.table_ld + j] = fresh(r, j);
     }
-    for (int r = rank * kPlanThreads + tid; r <= p.R; r += ctas * kPlanThreads)
+    for (int r = gtid; r < p.R; r += gsize) {
+        const int need = need_of(r);
+        p.held_out[r] = held[r] + (served(r, need) ? need : 0);
         p.cu_new[r] = cu[r];
-    // pages handed out: the served requests are those before the first that
-    // did not fit, so the sum ends at the last served one
-    int used = 0;
-    if (rank == 0) {
-        for (int r = tid; r < p.R; r += kPlanThreads) {
-            const int n = cu[r + 1] - cu[r], h = held[r];
-            if (n && base[r] >= 0)
-                used = max(used, base[r] + max(0, (int)(((long long)len[r] + n + p.page - 1) /
-                                                        p.page) - h));
-        }
-        used = __reduce_max_sync(~0u, used);
-        if (lane == 0)
-            part[tid >> 5] = used;
     }
+    if (gtid == 0) {
+        p.cu_new[p.R] = cu[p.R];
+        *p.free_count_out = avail - (int)used;
+    }
+    if (bits)
+        set_status(p.status, bits);
+}
+
+// The tokens' rows off the finished table: a request that was not served has
+// fewer pages than its last token needs, and none of its tokens gets a slot.
+constexpr int kTokenThreads = 256;
+
+__global__ void __launch_bounds__(kTokenThreads) token_kernel(const PlanProblem p)
+{
+    extern __shared__ int32_t cu[]; // [R + 1]
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int r = threadIdx.x; r <= p.R; r += kTokenThreads)
+        cu[r] = p.cu_new[r];
     __syncthreads();
-    if (rank == 0 && tid == 0) {
-        for (int w = 0; w < kPlanThreads / 32; ++w)
-            used = max(used, (int)part[w]);
-        *p.free_count_out = (int32_t)(avail - used);
+    const int T = cu[p.R];
+    int bits = 0;
+    for (int t = blockIdx.x * kTokenThreads + threadIdx.x; t < T; t += gridDim.x * kTokenThreads) {
+        const int r = place_in(cu, p.R, t), i = t - cu[r], len = p.lens[r];
+        const int j = ((uint32_t)len + i) / (uint32_t)p.page, off = len + i - j * p.page;
+        const bool ok = pages_of(len, cu[r + 1] - cu[r], p.page) <= p.held_out[r];
+        const int id = ok ? p.table[(long long)r * p.table_ld + j] : -1;
+        bits |= put_token(p, t, r, i, len, id, off, ok);
     }
     if (bits)
         set_status(p.status, bits);
 }
 
 // ---------------------------------------------------------------------------
-// The store: one thread per (token, head, eight pairs). The products and sums
-// of the rotation are rounded one by one (no contraction), so that a stored
-// value does not depend on how the compiler orders them.
+// The store: one CTA per token, D / 16 threads per head, each eight pairs of
+// several heads, so that a position's cosines and sines are read once and the
+// heads' loads are in flight together. The products and sums of the rotation
+// are rounded one by one (no contraction), so that a stored value does not
+// depend on how the compiler orders them. Bound by memory: 4001 tokens of 64
+// query and 8 key heads of 128 took 46 us with a thread per (head, eight pairs)
+// and its cosines, which were two thirds of the loads.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void unpack_bf16(const uint4 &u, float *f)
@@ -271,81 +332,101 @@ __device__ __forceinline__ uint2 pack_e4m3(const float *f, float scale)
 
 constexpr int kWriteThreads = 256;
 
+template <int D>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const WriteProblem p)
 {
-    const int D = p.cache.dim, half = D / 2, Hkv = p.cache.heads;
-    const int cpr = D / 16, heads = (p.q ? p.Hq : 0) + 2 * Hkv, per = heads * cpr;
+    constexpr int CPR = D / 16, STEP = kWriteThreads / CPR, BATCH = 3; // heads side by side, and at once
+    const int Hkv = p.cache.heads, heads = p.Hq + 2 * Hkv;
     grid_launch_dependents();
     grid_dependency_wait();
-    const int T = p.n_tokens ? min(max(*p.n_tokens, 0), p.T) : p.T;
-    const long long g = (long long)blockIdx.x * kWriteThreads + threadIdx.x;
-    const long long t = g / per;
-    if (p.n_tokens && g == 0 && *p.n_tokens != T)
-        set_status(p.status, SGQ_STATUS_BAD_COUNT);
-    if (t >= T)
-        return;
-    const int rest = (int)(g - t * per), c = rest % cpr;
-    int h = rest / cpr;
-    if (!p.q)
-        h += p.Hq;
-    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + Hkv;
-    if (!is_q)
-        h -= is_k ? p.Hq : p.Hq + Hkv;
-    const uint16_t *src = is_q   ? p.q + t * p.ld_q
-                          : is_k ? p.k + t * p.ld_k
-                                 : p.v + t * p.ld_v;
-    src += (long long)h * D + 8 * c;
-    float lo[8], hi[8];
-    unpack_bf16(*reinterpret_cast<const uint4 *>(src), lo);
-    unpack_bf16(*reinterpret_cast<const uint4 *>(src + half), hi);
+    const long long t = blockIdx.x;
+    if (p.n_tokens) {
+        const int n = *p.n_tokens;
+        if (t == 0 && threadIdx.x == 0 && (n < 0 || n > p.T))
+            set_status(p.status, SGQ_STATUS_BAD_COUNT);
+        if (t >= n)
+            return;
+    }
+    const int c = threadIdx.x % CPR;
+    float cs[8], sn[8];
     if (p.rope) {
         const int pos = p.pos[t];
         if (pos < 0 || pos >= p.rope_len) {
-            set_status(p.status, SGQ_STATUS_BAD_INDEX);
+            if (threadIdx.x == 0)
+                set_status(p.status, SGQ_STATUS_BAD_INDEX);
             return;
         }
-        if (is_q || is_k) {
-            const float4 *rc =
-                reinterpret_cast<const float4 *>(p.rope + (long long)pos * D + 8 * c);
-            const float4 *rs = reinterpret_cast<const float4 *>(
-                p.rope + (long long)pos * D + half + 8 * c);
-            const float4 c0 = rc[0], c1 = rc[1], s0 = rs[0], s1 = rs[1];
-            const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        const float4 *rc = reinterpret_cast<const float4 *>(p.rope + (long long)pos * D + 8 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = __fsub_rn(__fmul_rn(lo[i], cs[i]), __fmul_rn(hi[i], sn[i]));
-                const float b = __fadd_rn(__fmul_rn(hi[i], cs[i]), __fmul_rn(lo[i], sn[i]));
-                lo[i] = a;
-                hi[i] = b;
-            }
+        for (int i = 0; i < 2; ++i) {
+            const float4 a = rc[i], b = rc[D / 8 + i];
+            cs[4 * i] = a.x, cs[4 * i + 1] = a.y, cs[4 * i + 2] = a.z, cs[4 * i + 3] = a.w;
+            sn[4 * i] = b.x, sn[4 * i + 1] = b.y, sn[4 * i + 2] = b.z, sn[4 * i + 3] = b.w;
         }
     }
-    if (is_q) {
-        uint16_t *dst = p.q_out + t * p.ld_qo + (long long)h * D + 8 * c;
-        *reinterpret_cast<uint4 *>(dst) = pack_bf16(lo);
-        *reinterpret_cast<uint4 *>(dst + half) = pack_bf16(hi);
-        return;
-    }
+    // where keys and values go
     const long long slot = p.slots[t];
-    if (slot < 0 || slot >= (long long)p.cache.num_pages * p.cache.page) {
-        if (slot != -1)
-            set_status(p.status, SGQ_STATUS_BAD_INDEX);
-        return;
+    const bool store = slot >= 0 && slot < (long long)p.cache.num_pages * p.cache.page;
+    if (!store && slot != -1 && threadIdx.x == 0)
+        set_status(p.status, SGQ_STATUS_BAD_INDEX);
+    long long base = 0;
+    if (store) {
+        const long long pg = slot / p.cache.page;
+        base = pg * p.cache.page_stride + (slot - pg * p.cache.page) * p.cache.slot_stride + 8 * c;
     }
-    const long long pg = slot / p.cache.page, off = slot - pg * p.cache.page;
-    const long long e = pg * p.cache.page_stride + off * p.cache.slot_stride +
-                        h * p.cache.head_stride + 8 * c;
-    void *dst = is_k ? p.cache.k : p.cache.v;
-    if (p.cache.type == SGQ_TYPE_E4M3) {
-        const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
-        uint8_t *d8 = static_cast<uint8_t *>(dst) + e;
-        *reinterpret_cast<uint2 *>(d8) = pack_e4m3(lo, scale);
-        *reinterpret_cast<uint2 *>(d8 + half) = pack_e4m3(hi, scale);
-    } else {
-        uint16_t *d16 = static_cast<uint16_t *>(dst) + e;
-        *reinterpret_cast<uint4 *>(d16) = pack_bf16(lo);
-        *reinterpret_cast<uint4 *>(d16 + half) = pack_bf16(hi);
+    for (int h0 = threadIdx.x / CPR; h0 < heads; h0 += BATCH * STEP) {
+        uint4 raw[BATCH][2];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int h = h0 + b * STEP;
+            const uint16_t *src = h < p.Hq ? p.q + t * p.ld_q + (long long)h * D
+                                  : h < p.Hq + Hkv ? p.k + t * p.ld_k + (long long)(h - p.Hq) * D
+                                                   : p.v + t * p.ld_v + (long long)(h - p.Hq - Hkv) * D;
+            if (h < heads) {
+                raw[b][0] = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                raw[b][1] = *reinterpret_cast<const uint4 *>(src + D / 2 + 8 * c);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            int h = h0 + b * STEP;
+            if (h >= heads)
+                break;
+            float lo[8], hi[8];
+            unpack_bf16(raw[b][0], lo);
+            unpack_bf16(raw[b][1], hi);
+            if (p.rope && h < p.Hq + Hkv) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = __fsub_rn(__fmul_rn(lo[i], cs[i]), __fmul_rn(hi[i], sn[i]));
+                    const float y = __fadd_rn(__fmul_rn(hi[i], cs[i]), __fmul_rn(lo[i], sn[i]));
+                    lo[i] = x;
+                    hi[i] = y;
+                }
+            }
+            if (h < p.Hq) {
+                uint16_t *dst = p.q_out + t * p.ld_qo + (long long)h * D + 8 * c;
+                *reinterpret_cast<uint4 *>(dst) = pack_bf16(lo);
+                *reinterpret_cast<uint4 *>(dst + D / 2) = pack_bf16(hi);
+                continue;
+            }
+            if (!store)
+                continue;
+            const bool is_k = h < p.Hq + Hkv;
+            h -= is_k ? p.Hq : p.Hq + Hkv;
+            const long long e = base + h * p.cache.head_stride;
+            void *dst = is_k ? p.cache.k : p.cache.v;
+            if (p.cache.type == SGQ_TYPE_E4M3) {
+                const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
+                uint8_t *d8 = static_cast<uint8_t *>(dst) + e;
+                *reinterpret_cast<uint2 *>(d8) = pack_e4m3(lo, scale);
+                *reinterpret_cast<uint2 *>(d8 + D / 2) = pack_e4m3(hi, scale);
+            } else {
+                uint16_t *d16 = static_cast<uint16_t *>(dst) + e;
+                *reinterpret_cast<uint4 *>(d16) = pack_bf16(lo);
+                *reinterpret_cast<uint4 *>(d16 + D / 2) = pack_bf16(hi);
+            }
+        }
     }
 }
 
@@ -353,20 +434,22 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const WriteProblem
 
 cudaError_t launch_plan(const PlanProblem &p, int num_sms, cudaStream_t stream)
 {
-    (void)num_sms;
+    const bool rows = p.max_tokens <= kPlanCtas * kPlanThreads;
     int ctas = 1;
-    while (ctas < 8 && ctas * kPlanThreads < p.max_tokens)
+    while (ctas < kPlanCtas && ctas * kPlanThreads < std::max(p.R, p.max_tokens))
         ctas *= 2;
-    return launch_step(plan_kernel, dim3(ctas), kPlanThreads, (size_t)(4 * p.R + 1) * 4, ctas, stream, p);
+    const cudaError_t e = launch_step(plan_kernel, dim3(ctas), kPlanThreads, (size_t)(4 * p.R + 1) * 4, ctas, stream, p, rows);
+    if (rows || e != cudaSuccess)
+        return e;
+    const int grid = std::min(4 * num_sms, (p.max_tokens + kTokenThreads - 1) / kTokenThreads);
+    return launch_step(token_kernel, dim3(grid), kTokenThreads, (size_t)(p.R + 1) * 4, 1, stream, p);
 }
 
 cudaError_t launch_write(const WriteProblem &p, int num_sms, cudaStream_t stream)
 {
     (void)num_sms;
-    const long long per =
-        (long long)((p.q ? p.Hq : 0) + 2 * p.cache.heads) * (p.cache.dim / 16);
-    const long long grid = (p.T * per + kWriteThreads - 1) / kWriteThreads;
-    return launch_step(write_kernel, dim3((unsigned)grid), kWriteThreads, 0, 1, stream, p);
+    return p.cache.dim == 64 ? launch_step(write_kernel<64>, dim3(p.T), kWriteThreads, 0, 1, stream, p)
+                             : launch_step(write_kernel<128>, dim3(p.T), kWriteThreads, 0, 1, stream, p);
 }
 
 } // namespace sgq

@@ -176,7 +176,11 @@ template <int AT, int RT, int WT>
 cudaError_t launch_t(const NormProblem &p, cudaStream_t stream)
 {
     const int chunks = p.H / 8;
+#ifdef NK
+    const int k = chunks <= 1024*NK ? NK: 4;
+#else
     const int k = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+#endif
     const int block = ((chunks + k - 1) / k + 31) / 32 * 32;
     switch (k) {
     case 1: return launch_step(norm_kernel<AT, RT, WT, 1>, dim3(p.B), block, 0, 1, stream, p);
