@@ -1358,7 +1358,11 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
         return cudaErrorNotSupported;
     else if (!encode(&kmap, p.cache, p.cache.k, box) || !encode(&vmap, p.cache, p.cache.v, box))
         return cudaErrorInvalidValue;
-    const cudaError_t e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, p, kmap, vmap, box);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(attn_kernel<D, KV, MT>, C::SMEM, done);
+    if (e != cudaSuccess)
+        return e;
+    e = launch_step(attn_kernel<D, KV, MT>, dim3(grid), C::THREADS, C::SMEM, 1, stream, p, kmap, vmap, box);
     if (e != cudaSuccess)
         return e;
     return launch_step(join_kernel<D>, dim3(2 * grid), 32 * kJoinWarps, 0, 1, stream, p, MT);

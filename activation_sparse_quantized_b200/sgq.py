@@ -69,6 +69,8 @@ def _open(path):
 def load(path: str = LIB_PATH):
     """Load libsgq.so (raises if it has not been built)."""
     global _lib
+    if path is LIB_PATH and _lib is not None:
+        return _lib
     if path != LIB_PATH:
         return _open(path)
     with _lock:
@@ -130,7 +132,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:  # the current stream's handle (building a torch Stream object takes 3 us)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -345,21 +347,27 @@ def sgq_glu(gate, up, h, B, I, act, stream=None):
 # and that it lies on the current device.
 # --------------------------------------------------------------------------
 
-_INT32, _INT64, _FLOAT32, _BF16 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
-_WORDS = (torch.int32, torch.uint32)
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 _FLOATS = {torch.bfloat16: SGQ_TYPE_BF16, torch.float32: SGQ_TYPE_F32}
 _CACHES = {torch.bfloat16: SGQ_TYPE_BF16, torch.float8_e4m3fn: SGQ_TYPE_E4M3}
 
 
-def _dev(name, t, types, dev):
-    """The address of a tensor of one of the types on device ``dev`` (None passes)."""
+def _dev(name, t, dtype, dev):
+    """The address of a tensor of the type on device ``dev`` (None passes)."""
     if t is None:
         return None
-    if t.dtype not in types:
-        raise TypeError(f"{name}: element type {t.dtype}, expected {' or '.join(map(str, types))}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: element type {t.dtype}, expected {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected the current device, cuda:{dev}")
     return t.data_ptr()
+
+
+def _float_type(name, t):
+    """The C ABI's type of a bf16 or fp32 tensor."""
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"{name}: element type {t.dtype}, expected bfloat16 or float32")
+    return _FLOATS[t.dtype]
 
 
 class _CacheStruct(ctypes.Structure):
@@ -408,14 +416,13 @@ def sgq_cache_plan(lens, news, R, page, num_pages, table, table_ld, held, held_o
     """Block tables, slots and positions of the requests' new tokens, on the GPU."""
     d = torch.cuda.current_device()
     _check("sgq_cache_plan", load().sgq_cache_plan(
-        _dev("lens", lens, _INT32, d), _dev("news", news, _INT32, d), R, page, num_pages,
-        _dev("table", table, _INT32, d), table_ld, _dev("held", held, _INT32, d),
-        _dev("held_out", held_out, _INT32, d), _dev("free_pages", free_pages, _INT32, d),
-        _dev("free_count", free_count, _INT32, d),
-        _dev("free_count_out", free_count_out, _INT32, d), _dev("depth", depth, _INT32, d),
-        max_tokens, _dev("cu_new", cu_new, _INT32, d), _dev("slots", slots, _INT64, d),
-        _dev("pos", pos, _INT32, d), _dev("req", req, _INT32, d),
-        _dev("status", status, _INT32, d), _stream(stream)))
+        _dev("lens", lens, _I32, d), _dev("news", news, _I32, d), R, page, num_pages,
+        _dev("table", table, _I32, d), table_ld, _dev("held", held, _I32, d),
+        _dev("held_out", held_out, _I32, d), _dev("free_pages", free_pages, _I32, d),
+        _dev("free_count", free_count, _I32, d), _dev("free_count_out", free_count_out, _I32, d),
+        _dev("depth", depth, _I32, d), max_tokens, _dev("cu_new", cu_new, _I32, d),
+        _dev("slots", slots, _I64, d), _dev("pos", pos, _I32, d), _dev("req", req, _I32, d),
+        _dev("status", status, _I32, d), _stream(stream)))
 
 
 def sgq_cache_write(q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_len, slots,
@@ -424,9 +431,9 @@ def sgq_cache_write(q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_
     d = torch.cuda.current_device()
     _check("sgq_cache_write", load().sgq_cache_write(
         _dev("q", q, _BF16, d), ld_q, _dev("k", k, _BF16, d), ld_k, _dev("v", v, _BF16, d), ld_v,
-        T, _dev("n_tokens", n_tokens, _INT32, d), Hq, _dev("pos", pos, _INT32, d),
-        _dev("rope", rope, _FLOAT32, d), rope_len, _dev("slots", slots, _INT64, d),
-        _dev("q_out", q_out, _BF16, d), ld_qo, cache.on(d), _dev("status", status, _INT32, d),
+        T, _dev("n_tokens", n_tokens, _I32, d), Hq, _dev("pos", pos, _I32, d),
+        _dev("rope", rope, _F32, d), rope_len, _dev("slots", slots, _I64, d),
+        _dev("q_out", q_out, _BF16, d), ld_qo, cache.on(d), _dev("status", status, _I32, d),
         _stream(stream)))
 
 
@@ -439,12 +446,11 @@ def sgq_tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree,
     """Attention of each request's new tokens over its pages of ``cache`` (a Cache)."""
     d = torch.cuda.current_device()
     _check("sgq_tree_attn", load().sgq_tree_attn(
-        _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _INT32, d),
-        _dev("cu_new", cu_new, _INT32, d), _dev("table", table, _INT32, d), table_ld,
-        cache.on(d), _dev("tree", tree, _WORDS, d), tree_words, float(scale),
-        _dev("out", out, _BF16, d), ld_out, _dev("lse", lse, _FLOAT32, d),
-        _dev("workspace", workspace, _INT32, d), workspace.numel() * 4,
-        _dev("status", status, _INT32, d), _stream(stream)))
+        _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _I32, d),
+        _dev("cu_new", cu_new, _I32, d), _dev("table", table, _I32, d), table_ld, cache.on(d),
+        _dev("tree", tree, _I32, d), tree_words, scale, _dev("out", out, _BF16, d), ld_out,
+        _dev("lse", lse, _F32, d), _dev("workspace", workspace, _I32, d), workspace.nbytes,
+        _dev("status", status, _I32, d), _stream(stream)))
 
 
 def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_out, ld_ro,
@@ -452,17 +458,16 @@ def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_
     """The norms around a block with its gate and scaled residual; the element
     types of the C entry point (a_type, r_type, w_type) are the tensors' own."""
     d = torch.cuda.current_device()
-    w_types = {t.dtype for t in (w_post, gate, w_pre) if t is not None}
-    if len(w_types) > 1 or (resid_out is not None and resid_out.dtype != resid.dtype):
-        raise TypeError("sgq_residual_norm: w_post, gate and w_pre share one element type, "
-                        "as do resid and resid_out")
+    w = w_pre if w_pre is not None else w_post if w_post is not None else gate
+    at, rt = None if a is None else a.dtype, resid.dtype
+    wt = None if w is None else w.dtype
     _check("sgq_residual_norm", load().sgq_residual_norm(
-        _dev("a", a, _FLOATS, d), ld_a, _FLOATS[a.dtype] if a is not None else SGQ_TYPE_F32,
-        _dev("w_post", w_post, _FLOATS, d), _dev("gate", gate, _FLOATS, d), ld_gate,
-        float(scale), _dev("resid", resid, _FLOATS, d), ld_r, _FLOATS[resid.dtype],
-        _dev("resid_out", resid_out, _FLOATS, d), ld_ro, _dev("w_pre", w_pre, _FLOATS, d),
-        _FLOATS[w_types.pop()] if w_types else SGQ_TYPE_F32, float(w_offset),
-        _dev("x", x, _BF16, d), ld_x, B, H, float(eps), _stream(stream)))
+        _dev("a", a, at, d), ld_a, SGQ_TYPE_F32 if a is None else _float_type("a", a),
+        _dev("w_post", w_post, wt, d), _dev("gate", gate, wt, d), ld_gate, scale,
+        _dev("resid", resid, rt, d), ld_r, _float_type("resid", resid),
+        _dev("resid_out", resid_out, rt, d), ld_ro, _dev("w_pre", w_pre, wt, d),
+        SGQ_TYPE_F32 if w is None else _float_type("w_pre, w_post and gate", w), w_offset,
+        _dev("x", x, _BF16, d), ld_x, B, H, eps, _stream(stream)))
 
 
 # --------------------------------------------------------------------------

@@ -127,10 +127,12 @@ def test_status_strings(lib):
 def test_binding_refuses_types_devices_and_shapes():
     cpu = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(TypeError, match="lens"):
-        sgq._dev("lens", cpu.float(), (torch.int32,), 0)
+        sgq._dev("lens", cpu.float(), torch.int32, 0)
     with pytest.raises(ValueError, match="current device"):
-        sgq._dev("lens", cpu, (torch.int32,), 0)
-    assert sgq._dev("tree", None, (torch.int32,), 0) is None
+        sgq._dev("lens", cpu, torch.int32, 0)
+    assert sgq._dev("tree", None, torch.int32, 0) is None
+    with pytest.raises(TypeError, match="resid"):
+        sgq._float_type("resid", cpu)
     k = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         sgq.Cache(k, k[:2])
