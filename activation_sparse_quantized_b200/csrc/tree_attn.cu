@@ -912,6 +912,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 // The weights are rounded to the values' type for the product
                 // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
                 // small ones, 2^-25); their sum l is of the unrounded ones.
+                // (A third of the exponentials by polynomial on the FMA pipe did
+                // not change 12 wide trees' 175 us, half of them made it 184.)
                 auto weigh = [&](const uint32_t *s, float ref, uint32_t *w, float2 *sum) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -1096,28 +1098,32 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     const int wtid = both ? tid : gtid, wth = both ? 2 * kGroup : kGroup;
                     const int used = min(32, sg.n * G - sg.rt * MT);
                     const float4 *a = out + (both ? 0 : grp) * (C::P1 / 16);
+                    // 2^lg float4 of a row at a time: all of up to 16 rows
+                    const int lg = D == 128 && used <= 16 ? 5 : 4, rows_lg = lg == 5 ? 4 : 5;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 64) {
+                    for (int c0 = 0; c0 < D; c0 += 4 << lg) {
                         if (quad == 0)
-#pragma unroll
-                            for (int c = 0; c < 64; c += 32) {
+#pragma unroll 1
+                            for (int c = 0; c < 4 << lg; c += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(tO + c0 + c, o);
                                 tmem_ld_wait(o);
+                                if (row < used)
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    out[grp * (C::P1 / 16) + row * 16 + ((c / 4 + e) ^ (row & 7))] =
-                                        make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                                    __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                                    for (int e = 0; e < 8; ++e)
+                                        out[grp * (C::P1 / 16) + (row << lg) + ((c / 4 + e) ^ (row & 7))] =
+                                            make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                        __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                                __syncwarp();
                             }
                         sync();
                         // rows next to each other in a part, columns in the output
 #pragma unroll 2
                         for (int k = wtid; k < 512; k += wth) {
-                            const int r = sg.whole ? k >> 4 : k & 31, e = sg.whole ? k & 15 : k >> 5;
+                            const int r = sg.whole ? k >> lg : k & ((1 << rows_lg) - 1), e = sg.whole ? k & ((1 << lg) - 1) : k >> rows_lg;
                             if (r >= used)
                                 continue;
-                            const int at = r * 16 + (e ^ (r & 7));
+                            const int at = (r << lg) + (e ^ (r & 7));
                             float4 x = a[at];
                             if (both) {
                                 const float4 y = a[C::P1 / 16 + at];
