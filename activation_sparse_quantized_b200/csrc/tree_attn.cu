@@ -1216,16 +1216,17 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
 }
 
 // Joins the parts of the items that several CTAs worked on, in key order. A unit
-// is 8 rows of 16 columns (a lane: one row, four columns); the CTAs of an item
-// share its units, CTA c0 + x taking units x, x + parts, ..., and a CTA's warps
-// share the parts of each where there are fewer units than warps.
-constexpr int kJoinWarps = 16;
+// is 8 rows of 64 columns (a lane: one row, sixteen columns, four by four); the
+// CTAs of an item share its units, CTA c0 + x taking units x, x + parts, ...,
+// and a CTA's warps share the parts of each where there are fewer units than
+// warps. Bound by the trips to L2: four parts' loads are on their way at once.
+constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem p, int MT)
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) join_kernel(const AttnProblem p, int MT)
 {
-    constexpr int BATCH = 4;
-    __shared__ float4 s_o[kJoinWarps][32];
+    constexpr int BATCH = 4, VEC = 4;
+    __shared__ float4 s_o[kJoinWarps][VEC][32];
     __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_launch_dependents();
@@ -1235,20 +1236,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
         return;
     const int G = p.Hq / p.cache.heads, first = (int)(blockIdx.x >> 1) - sp.c0;
     const int rows = (int)min((long long)MT, (long long)sp.n * G - (long long)sp.rt * MT);
-    const int units = (rows + 7) / 8 * (D / 16);
+    const int units = (rows + 7) / 8 * (D / 64);
     const int mine = units > first ? (units - first + sp.parts - 1) / sp.parts : 0;
     int wpu = kJoinWarps; // warps per unit
     while (wpu > 1 && wpu * mine > kJoinWarps)
         wpu >>= 1;
     for (int k0 = 0; k0 < mine; k0 += kJoinWarps / wpu) {
         const int k = k0 + warp / wpu, u = first + k * sp.parts;
-        const int row = u / (D / 16) * 8 + (lane & 7), c4 = u % (D / 16) * 4 + (lane >> 3);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int row = u / (D / 64) * 8 + (lane & 7), c4 = u % (D / 64) * 16 + (lane >> 3);
+        float4 o[VEC] = {};
         float m = -INFINITY, l = 0.0f;
         if (k < mine && row < rows) {
             for (int b = warp % wpu; b < sp.parts; b += BATCH * wpu) {
                 float pm[BATCH], pl[BATCH];
-                float4 v[BATCH];
+                float4 v[BATCH][VEC];
 #pragma unroll
                 for (int e = 0; e < BATCH; ++e) {
                     const int c = b + e * wpu;
@@ -1256,26 +1257,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
                     const float *part = part_of(p, sp.c0 + (in ? c : 0), !in || c == 0, MT, D);
                     pm[e] = in ? part[MT * D + row] : -INFINITY;
                     pl[e] = in ? part[MT * D + MT + row] : 0.0f;
-                    v[e] = in ? reinterpret_cast<const float4 *>(part)[c4 * MT + row] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x)
+                        v[e][x] = in ? reinterpret_cast<const float4 *>(part)[(c4 + 4 * x) * MT + row] : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 float top = m;
 #pragma unroll
                 for (int e = 0; e < BATCH; ++e)
                     top = fmaxf(top, pm[e]);
                 const float ref = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - ref);
-                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-                l *= f;
                 m = top;
+                l *= f;
+#pragma unroll
+                for (int x = 0; x < VEC; ++x)
+                    o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
 #pragma unroll
                 for (int e = 0; e < BATCH; ++e) {
                     const float w = exp2_fast(pm[e] - ref);
-                    o = make_float4(o.x + v[e].x * w, o.y + v[e].y * w, o.z + v[e].z * w, o.w + v[e].w * w);
                     l += pl[e] * w;
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x)
+                        o[x] = make_float4(o[x].x + v[e][x].x * w, o[x].y + v[e][x].y * w, o[x].z + v[e][x].z * w, o[x].w + v[e][x].w * w);
                 }
             }
         }
         if (wpu > 1) {
-            s_o[warp][lane] = o;
+#pragma unroll
+            for (int x = 0; x < VEC; ++x)
+                s_o[warp][x][lane] = o[x];
             s_m[warp][lane] = m;
             s_l[warp][lane] = l;
             __syncthreads();
@@ -1284,15 +1293,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
                 for (int w = 1; w < wpu; ++w)
                     top = fmaxf(top, s_m[warp + w][lane]);
                 const float ref = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - ref);
-                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-                l *= f;
                 m = top;
-#pragma unroll 4
+                l *= f;
+#pragma unroll
+                for (int x = 0; x < VEC; ++x)
+                    o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
                 for (int w = 1; w < wpu; ++w) {
                     const float e = exp2_fast(s_m[warp + w][lane] - ref);
-                    const float4 v = s_o[warp + w][lane];
-                    o = make_float4(o.x + v.x * e, o.y + v.y * e, o.z + v.z * e, o.w + v.w * e);
                     l += s_l[warp + w][lane] * e;
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x) {
+                        const float4 v = s_o[warp + w][x][lane];
+                        o[x] = make_float4(o[x].x + v.x * e, o[x].y + v.y * e, o[x].z + v.z * e, o[x].w + v.w * e);
+                    }
                 }
             }
             __syncthreads();
@@ -1301,8 +1314,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnProblem
             const int g = sp.rt * MT + row, ti = g / G, hq = sp.h * G + g - ti * G;
             const long long t = sp.tok + ti;
             const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
-            *reinterpret_cast<uint2 *>(p.out + t * p.ld_out + (long long)hq * D + 4 * c4) =
-                make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+            uint16_t *out = p.out + t * p.ld_out + (long long)hq * D + 4 * c4;
+#pragma unroll
+            for (int x = 0; x < VEC; ++x)
+                *reinterpret_cast<uint2 *>(out + 16 * x) =
+                    make_uint2(pack2<false>(o[x].x * inv, o[x].y * inv), pack2<false>(o[x].z * inv, o[x].w * inv));
             if (p.lse && c4 == 0)
                 p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
