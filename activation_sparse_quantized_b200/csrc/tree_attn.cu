@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        // The next kernel may start: not before this CTA has its tensor memory, which a
+        // CTA of that kernel would hold while it waits for this one.
+        grid_launch_dependents();
     } else if (warp == kKeys && lane == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             bar_init(bFull + 8 * s, box ? 1 : 32); // one bulk copy's thread, or the lanes of a warp
@@ -205,7 +208,6 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         bar_init(bQFree, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    grid_launch_dependents();
     grid_dependency_wait();
 
     // The requests' costs, their sum U, and this CTA's run of [0, U).
