@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 nt = -nt;
             }
             bar_wait(bFull + 8 * kr.s, kr.ph, ok);
-            fence_async_smem(); // the copies' writes, for the product's reads
+            if (!box)
+                fence_async_smem(); // the copies' writes, for the product's reads
             __syncwarp();
             tc_after();
             const uint32_t d = tmem + buf * kTile, ka = sKV + kr.s * slot_bytes;
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             const uint32_t vfull = C::F8 ? bVFull + 8 * (i & 1) : bFull + 8 * vr.s;
             bar_wait(vfull, C::F8 ? (i >> 1) & 1 : vr.ph, ok);
             bar_wait(bP + 8 * buf, p_ph, ok);
-            if (!C::F8)
+            if (!C::F8 && !box)
                 fence_async_smem();
             __syncwarp();
             tc_after();
