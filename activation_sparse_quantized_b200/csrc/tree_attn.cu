@@ -90,7 +90,7 @@ struct Cfg {
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
     static constexpr int ROWB = F8 ? D : 2 * D, CPR = ROWB / 16; // bytes, 16-byte chunks of a key
     static constexpr int OUT1 = 32 * 64, OUT = MT == 128 ? 8 * OUT1 : 0; // 16 columns of a warp's rows, for the other group
-    static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 2;
+    static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 3;
     static constexpr int SMEM = 1024 + Q + P + KV_BYTES + NV * SLOT + OUT + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
     // copies run ahead of the softmax by the ring's tiles, 8-bit ones by NV more and the
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     const uint32_t bFull = sOut + C::OUT, bEmpty = bFull + 8 * C::SLOTS;
     const uint32_t bVFull = bEmpty + 8 * C::SLOTS, bVEmpty = bVFull + 8 * C::NV;
     const uint32_t bS = bVEmpty + 8 * C::NV, bP = bS + 16, bO = bP + 16;
-    const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8;
+    const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8, bDone = bQFree + 8;
     // the ring of copies: keys in one slot, values in the next
     constexpr uint32_t slot_bytes = kTile * C::ROWB;
     constexpr int slots = C::SLOTS;
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         }
         bar_init(bQ, C::F8 || C::FEW ? C::QW : 32 * C::QW);
         bar_init(bQFree, 1);
+        bar_init(bDone, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_dependency_wait();
@@ -388,6 +389,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     bar_wait(bEmpty + 8 * ring.s, ring.ph ^ 1, ok);
                     __syncwarp();
                     const uint32_t full = bFull + 8 * ring.s, dst = sKV + ring.s * slot_bytes;
+                    if (!__all_sync(~0u, ok)) // the slot may be in use
+                        break;
                     if (lane == 0)
                         bar_expect(full, kTile * C::ROWB);
                     __syncwarp();
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             if (left == 0 && !ended) {
                 bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
                 __syncwarp();
-                left = __all_sync(~0u, led) ? s_seg[seg.s].nt : 0;
+                left = (int)__reduce_max_sync(~0u, __all_sync(~0u, led) ? (unsigned)s_seg[seg.s].nt : 0u);
                 seg.step(1, kRing);
                 ended = left == 0;
                 nt = -left; // its Q has not been waited for
@@ -602,17 +605,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 nt_i = abs(nt);
             }
         }
-        // every product is complete before the tensor memory is freed
+        // every product and every arrival is complete before the CTA ends
         bool done = true;
-        if constexpr (C::TWO) {
-            for (int b = 0; b < 2 && i > 0; ++b)
-                bar_wait(bO + 8 * b, (i - 1) & 1, done);
-        } else {
-            if (i >= 2)
-                bar_wait(bO + 8 * (i & 1), ((i - 2) >> 1) & 1, done);
-            if (i >= 1)
-                bar_wait(bO + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, done);
-        }
+        tc_commit(bDone, lead);
+        bar_wait(bDone, 0, done);
         ok = ok && done;
         __syncwarp();
     } else if (warp >= kQ && warp < C::kV) {
