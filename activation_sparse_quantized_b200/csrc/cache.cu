@@ -30,7 +30,7 @@ namespace {
 //
 // More tokens than the cluster has threads go to a second kernel over all SMs,
 // which reads the slots off the finished table: 16 requests with 136 tokens
-// take 4.4 us on the one kernel, and 2000 requests with 301,000 tokens 10 us on
+// take 4.6 us on the one kernel, and 2000 requests with 301,000 tokens 16.8 us on
 // two, 75 us on one.
 // ---------------------------------------------------------------------------
 
@@ -291,9 +291,10 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const PlanProblem 
 // several heads, so that a position's cosines and sines are read once and the
 // heads' loads are in flight together. The products and sums of the rotation
 // are rounded one by one (no contraction), so that a stored value does not
-// depend on how the compiler orders them. Bound by memory: 4001 tokens of 64
-// query and 8 key heads of 128 took 46 us with a thread per (head, eight pairs)
-// and its cosines, which were two thirds of the loads.
+// depend on how the compiler orders them. 4001 tokens of 64 query and 8 key heads
+// of 128 are bound by memory: 35.7 us, 4.7 TB/s; a thread per (head, eight pairs)
+// with its own cosines, two thirds of the loads, took 46. 16 tokens are bound by
+// the chain of loads: 2.3 us.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void unpack_bf16(const uint4 &u, float *f)
@@ -331,28 +332,46 @@ __device__ __forceinline__ uint2 pack_e4m3(const float *f, float scale)
 }
 
 constexpr int kWriteThreads = 512; // at most
-constexpr int kWriteBatch = 4;     // heads of a thread at once
+constexpr int kWriteBatch = 4;     // heads of a thread at once, with many tokens
 
-template <int D>
+template <int D, int BATCH>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const WriteProblem p)
 {
-    constexpr int CPR = D / 16, BATCH = kWriteBatch;
+    constexpr int CPR = D / 16;
+    constexpr bool EARLY = BATCH == 1;
     const int STEP = blockDim.x / CPR; // heads side by side
     const int Hkv = p.cache.heads, heads = p.Hq + 2 * Hkv;
     grid_launch_dependents();
     grid_dependency_wait();
+    // With one head a thread every load that needs no other's result is on its way
+    // before the first wait (rows behind the last token are read, and not used). With
+    // more the registers cost more than that brings: 38.2 us against 35.7.
     const long long t = blockIdx.x;
-    if (p.n_tokens) {
-        const int n = *p.n_tokens;
-        if (t == 0 && threadIdx.x == 0 && (n < 0 || n > p.T))
-            set_status(p.status, SGQ_STATUS_BAD_COUNT);
-        if (t >= n)
-            return;
-    }
     const int c = threadIdx.x % CPR;
+    uint4 raw[BATCH][2];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int h = h0 + b * STEP;
+            const uint16_t *src = h < p.Hq ? p.q + t * p.ld_q + (long long)h * D
+                                  : h < p.Hq + Hkv ? p.k + t * p.ld_k + (long long)(h - p.Hq) * D
+                                                   : p.v + t * p.ld_v + (long long)(h - p.Hq - Hkv) * D;
+            if (h < heads) {
+                raw[b][0] = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                raw[b][1] = *reinterpret_cast<const uint4 *>(src + D / 2 + 8 * c);
+            }
+        }
+    };
+    const int n = p.n_tokens ? *p.n_tokens : p.T, pos = p.rope ? p.pos[t] : 0;
+    const long long slot = p.slots[t];
+    if (EARLY)
+        load(threadIdx.x / CPR);
+    if (t == 0 && threadIdx.x == 0 && (n < 0 || n > p.T))
+        set_status(p.status, SGQ_STATUS_BAD_COUNT);
+    if (t >= n)
+        return;
     float cs[8], sn[8];
     if (p.rope) {
-        const int pos = p.pos[t];
         if (pos < 0 || pos >= p.rope_len) {
             if (threadIdx.x == 0)
                 set_status(p.status, SGQ_STATUS_BAD_INDEX);
@@ -367,7 +386,6 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const WriteProblem
         }
     }
     // where keys and values go
-    const long long slot = p.slots[t];
     const bool store = slot >= 0 && slot < (long long)p.cache.num_pages * p.cache.page;
     if (!store && slot != -1 && threadIdx.x == 0)
         set_status(p.status, SGQ_STATUS_BAD_INDEX);
@@ -377,18 +395,8 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const WriteProblem
         base = pg * p.cache.page_stride + (slot - pg * p.cache.page) * p.cache.slot_stride + 8 * c;
     }
     for (int h0 = threadIdx.x / CPR; h0 < heads; h0 += BATCH * STEP) {
-        uint4 raw[BATCH][2];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int h = h0 + b * STEP;
-            const uint16_t *src = h < p.Hq ? p.q + t * p.ld_q + (long long)h * D
-                                  : h < p.Hq + Hkv ? p.k + t * p.ld_k + (long long)(h - p.Hq) * D
-                                                   : p.v + t * p.ld_v + (long long)(h - p.Hq - Hkv) * D;
-            if (h < heads) {
-                raw[b][0] = *reinterpret_cast<const uint4 *>(src + 8 * c);
-                raw[b][1] = *reinterpret_cast<const uint4 *>(src + D / 2 + 8 * c);
-            }
-        }
+        if (!EARLY || h0 >= STEP)
+            load(h0);
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             int h = h0 + b * STEP;
@@ -453,13 +461,14 @@ cudaError_t launch_plan(const PlanProblem &p, int num_sms, cudaStream_t stream)
 cudaError_t launch_write(const WriteProblem &p, int num_sms, cudaStream_t stream)
 {
     // as many threads as take all the heads at once, in whole warps; with few
-    // tokens, where latency counts, one head each (16 tokens of 48 heads: 2.8 us
-    // against 3.8)
-    const int heads = p.Hq + 2 * p.cache.heads, batch = p.T < 2 * num_sms ? 1 : kWriteBatch;
+    // tokens, where latency counts, one head each
+    const bool few = p.T < 2 * num_sms;
+    const int heads = p.Hq + 2 * p.cache.heads, batch = few ? 1 : kWriteBatch;
     const int threads = (heads + batch - 1) / batch * (p.cache.dim / 16);
     const int block = std::min(kWriteThreads, (threads + 31) / 32 * 32);
-    return p.cache.dim == 64 ? launch_step(write_kernel<64>, dim3(p.T), block, 0, 1, stream, p)
-                             : launch_step(write_kernel<128>, dim3(p.T), block, 0, 1, stream, p);
+    const auto kern = p.cache.dim == 64 ? (few ? write_kernel<64, 1> : write_kernel<64, kWriteBatch>)
+                                        : (few ? write_kernel<128, 1> : write_kernel<128, kWriteBatch>);
+    return launch_step(kern, dim3(p.T), block, 0, 1, stream, p);
 }
 
 } // namespace sgq
