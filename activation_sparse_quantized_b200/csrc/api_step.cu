@@ -4,6 +4,7 @@
 // here allocates, frees or synchronises.
 #include "sgq_launch.h"
 
+#include <cmath>
 #include <cuda_runtime.h>
 
 namespace {
@@ -18,7 +19,8 @@ int finish(cudaError_t e)
     return e == cudaSuccess ? SGQ_OK : sgq::record_cuda_error(e);
 }
 
-constexpr long long kMaxStride = 1ll << 40; // elements
+constexpr long long kMaxStride = 1ll << 40;      // elements
+constexpr long long kMaxCacheStride = 1ll << 38; // elements; a tensor map takes less than 2^40 bytes
 
 // A row stride of 2- or 4-byte elements: rows start on 16 bytes and do not overlap.
 bool stride_ok(long long ld, long long width, int elem_bytes)
@@ -37,8 +39,8 @@ int check_cache(const sgq_cache *c)
         return SGQ_ERR_SHAPE;
     const long long unit = c->type == SGQ_TYPE_E4M3 ? 16 : 8; // elements in 16 bytes
     if (c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0 ||
-        c->page_stride > kMaxStride || c->slot_stride > kMaxStride ||
-        c->head_stride > kMaxStride)
+        c->page_stride > kMaxCacheStride || c->slot_stride > kMaxCacheStride ||
+        c->head_stride > kMaxCacheStride)
         return SGQ_ERR_SHAPE;
     if (c->page_stride % unit || c->slot_stride % unit || c->head_stride % unit)
         return SGQ_ERR_ALIGN;
@@ -170,7 +172,8 @@ int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int
     const long long D = cache_host->dim, Hkv = cache_host->heads;
     if (T < 1 || Hq < Hkv || Hq % Hkv != 0 || table_ld < 1 ||
         (long long)table_ld * cache_host->page > (1ll << 30) ||
-        Hq > 32768 || (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))))
+        Hq > 32768 || (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))) ||
+        !(fabsf(scale) * cache_host->k_scale <= 1e37f)) // (not a number: refused)
         return SGQ_ERR_SHAPE;
     if (!q || !lens || !cu_new || !table || !out || !workspace)
         return SGQ_ERR_NULL;

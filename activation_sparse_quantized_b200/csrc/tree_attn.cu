@@ -19,12 +19,13 @@
 // directly.
 //
 // Both products are tcgen05.mma of 128 rows and 128 keys. The warps:
-//  * one walks the run and copies keys, one copies values, row by row into a
-//    ring, two slots per 128 keys, in the products' swizzled layout; what lies
-//    behind a segment's keys, and bad pages, is filled with zeros. The copies
-//    are cp.async, 16 bytes a lane: by bulk tensor copies, a box per page and
-//    128 bytes, the issue of the boxes set the pace (70 to 110 ns a box and
-//    warp: 1.15 us per 128 8-bit keys in pages of 24, where the bytes take 0.2);
+//  * one walks the run and copies keys, one copies values, into a ring of 128-key
+//    slots in the products' swizzled layout; what lies behind a segment's keys,
+//    and bad pages, is filled with zeros. The copies are bulk tensor copies, a
+//    box per 128 bytes of so many slots of a page, where a box has 512 bytes at
+//    least, else cp.async of 16 bytes a lane. A box takes its warp some 40 ns
+//    (11 requests of 8-bit keys in pages of 24, 16 boxes of 512 bytes a slot: 75 us,
+//    in pages of 128 70);
 //  * one thread issues S = Q K^T (both from shared memory) into one of two
 //    accumulators, one tile ahead and across segments, and O += P V with P
 //    read from tensor memory, where it takes S's place;
@@ -646,75 +647,75 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 }
                 cp_async_arrive(bQ);
                 free_ph ^= 1;
-                continue;
-            }
+            } else {
 #pragma unroll 1
-            for (int k0 = 0; k0 < ALL; k0 += N) {
-                uint4 v[N];
+                for (int k0 = 0; k0 < ALL; k0 += N) {
+                    uint4 v[N];
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * QT, x = rem0 + idx / CH;
-                    const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ti < n)
-                        v[k] = *reinterpret_cast<const uint4 *>(p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D +
-                                                                8 * (idx % CH));
-                }
-                if (k0 == 0)
-                    bar_wait(bQFree, free_ph, ok); // the last segment's scores are done
-                __syncwarp();
+                    for (int k = 0; k < N; ++k) {
+                        const int idx = ct + (k0 + k) * QT, x = rem0 + idx / CH;
+                        const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
+                        v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (ti < n)
+                            v[k] = *reinterpret_cast<const uint4 *>(p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D +
+                                                                    8 * (idx % CH));
+                    }
+                    if (k0 == 0)
+                        bar_wait(bQFree, free_ph, ok); // the last segment's scores are done
+                    __syncwarp();
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const int idx = ct + (k0 + k) * QT, qr = idx / CH, c = idx % CH;
-                    uint8_t *dst = smem + (C::TWO ? (qr >> 7) * C::Q1 : 0);
-                    const int r = C::TWO ? qr & 127 : qr;
-                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    if constexpr (C::F8) {
-                        float f[8], mx = 0.0f;
+                    for (int k = 0; k < N; ++k) {
+                        const int idx = ct + (k0 + k) * QT, qr = idx / CH, c = idx % CH;
+                        uint8_t *dst = smem + (C::TWO ? (qr >> 7) * C::Q1 : 0);
+                        const int r = C::TWO ? qr & 127 : qr;
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        if constexpr (C::F8) {
+                            float f[8], mx = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            f[2 * e] = __uint_as_float(w[e] << 16);
-                            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                            mx = fmaxf(mx, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                            for (int e = 0; e < 4; ++e) {
+                                f[2 * e] = __uint_as_float(w[e] << 16);
+                                f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                                mx = fmaxf(mx, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                            }
+#pragma unroll
+                            for (int o = CH / 2; o; o >>= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                            // both the power and its inverse are normal fp32 numbers
+                            const int up = min(max(7 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
+                            const float mul = pow2f(up);
+                            uint32_t part[2][2];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 x = make_float2(f[2 * e] * mul, f[2 * e + 1] * mul);
+                                const uint32_t hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                                const uint32_t h2 = e4m3x2_to_f16x2(hi);
+                                const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                                part[0][e >> 1] = e & 1 ? part[0][e >> 1] | hi << 16 : hi;
+                                part[1][e >> 1] = e & 1 ? part[1][e >> 1] | lo << 16 : lo;
+                            }
+                            if (c == 0)
+                                s_f[segs & 3][qr] = pow2f(-up);
+#pragma unroll
+                            for (int cp = 0; cp < C::COPIES; ++cp)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    *reinterpret_cast<uint2 *>(dst + e * C::SUB + op_off(r + cp * MT, c >> 1) + 8 * (c & 1)) =
+                                        make_uint2(part[e][0], part[e][1]);
+                        } else {
+#pragma unroll
+                            for (int cp = 0; cp < C::COPIES; ++cp)
+                                *reinterpret_cast<uint4 *>(dst + op_off(r + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-#pragma unroll
-                        for (int o = CH / 2; o; o >>= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                        // both the power and its inverse are normal fp32 numbers
-                        const int up = min(max(7 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
-                        const float mul = pow2f(up);
-                        uint32_t part[2][2];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 x = make_float2(f[2 * e] * mul, f[2 * e + 1] * mul);
-                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-                            const uint32_t h2 = e4m3x2_to_f16x2(hi);
-                            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
-                            part[0][e >> 1] = e & 1 ? part[0][e >> 1] | hi << 16 : hi;
-                            part[1][e >> 1] = e & 1 ? part[1][e >> 1] | lo << 16 : lo;
-                        }
-                        if (c == 0)
-                            s_f[segs & 3][qr] = pow2f(-up);
-#pragma unroll
-                        for (int cp = 0; cp < C::COPIES; ++cp)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<uint2 *>(dst + e * C::SUB + op_off(r + cp * MT, c >> 1) + 8 * (c & 1)) =
-                                    make_uint2(part[e][0], part[e][1]);
-                    } else {
-#pragma unroll
-                        for (int cp = 0; cp < C::COPIES; ++cp)
-                            *reinterpret_cast<uint4 *>(dst + op_off(r + cp * MT, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                free_ph ^= 1;
+                ++segs;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(bQ);
             }
-            free_ph ^= 1;
-            ++segs;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(bQ);
         }
     } else if (warp >= C::kV) {
         // ---- the values next to the end, 8-bit values -> fp16 -------------------

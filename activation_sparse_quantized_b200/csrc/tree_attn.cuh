@@ -58,8 +58,9 @@ __device__ __forceinline__ int cta_of(long long U, long long u, int C)
 
 // A CTA's share of an item that several CTAs work on, c0 to c0 + parts - 1
 // (parts = 0: none): the one it goes on with ([0]) and the one it starts ([1]).
-struct __align__(32) Split {
-    int parts, c0, tok, n, h, rt;
+// 16 bytes are what a workspace is aligned to.
+struct __align__(16) Split {
+    int parts, c0, tok, n, h, rt, pad[2];
 };
 
 // The part that CTA c leaves of either: D sums of MT rows, four of a row side by

@@ -389,19 +389,23 @@ class Cache:
     """
 
     def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        if k.dim() != 4 or v.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("Cache: k and v must be [num_pages, page, heads, dim] alike")
         if k.dtype not in _CACHES:
             raise TypeError(f"Cache: element type {k.dtype}, expected bfloat16 or float8_e4m3fn")
-        if k.stride(3) != 1:
+        if k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("Cache: k and v must be contiguous along dim")
         if k.get_device() != v.get_device():
             raise ValueError("Cache: k and v must be on one device")
+        # a dimension of one entry is never stepped over, whatever its stride says
+        strides, other = (tuple(s if n > 1 else t.shape[3] for s, n in zip(t.stride(), t.shape)) for t in (k, v))
+        if strides != other:
+            raise ValueError("Cache: k and v must have the same strides")
         self.k, self.v = k, v
         self.device = k.get_device()
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _CACHES[k.dtype], k.shape[1],
-                                   k.shape[0], k.shape[2], k.shape[3], k.stride(0), k.stride(1),
-                                   k.stride(2), float(k_scale), float(v_scale))
+                                   k.shape[0], k.shape[2], k.shape[3], *strides[:3], float(k_scale),
+                                   float(v_scale))
         self.ptr = ctypes.addressof(self.struct)
 
     def on(self, dev):
@@ -449,7 +453,8 @@ def sgq_tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree,
         _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _I32, d),
         _dev("cu_new", cu_new, _I32, d), _dev("table", table, _I32, d), table_ld, cache.on(d),
         _dev("tree", tree, _I32, d), tree_words, scale, _dev("out", out, _BF16, d), ld_out,
-        _dev("lse", lse, _F32, d), _dev("workspace", workspace, _I32, d), workspace.nbytes,
+        _dev("lse", lse, _F32, d), _dev("workspace", workspace, _I32, d),
+        0 if workspace is None else workspace.nbytes,
         _dev("status", status, _I32, d), _stream(stream)))
 
 
@@ -459,12 +464,12 @@ def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_
     types of the C entry point (a_type, r_type, w_type) are the tensors' own."""
     d = torch.cuda.current_device()
     w = w_pre if w_pre is not None else w_post if w_post is not None else gate
-    at, rt = None if a is None else a.dtype, resid.dtype
+    at, rt = None if a is None else a.dtype, None if resid is None else resid.dtype
     wt = None if w is None else w.dtype
     _check("sgq_residual_norm", load().sgq_residual_norm(
         _dev("a", a, at, d), ld_a, SGQ_TYPE_F32 if a is None else _float_type("a", a),
         _dev("w_post", w_post, wt, d), _dev("gate", gate, wt, d), ld_gate, scale,
-        _dev("resid", resid, rt, d), ld_r, _float_type("resid", resid),
+        _dev("resid", resid, rt, d), ld_r, SGQ_TYPE_F32 if resid is None else _float_type("resid", resid),
         _dev("resid_out", resid_out, rt, d), ld_ro, _dev("w_pre", w_pre, wt, d),
         SGQ_TYPE_F32 if w is None else _float_type("w_pre, w_post and gate", w), w_offset,
         _dev("x", x, _BF16, d), ld_x, B, H, eps, _stream(stream)))

@@ -64,7 +64,7 @@ extern "C" {
 #define SGQ_STATUS_NONFINITE_W  1  /* sgq_pack: W holds NaN or Inf (that group packed as zeros) */
 #define SGQ_STATUS_BAD_INDEX    2  /* an index (channel, page, slot, position) out of range was skipped */
 #define SGQ_STATUS_BAD_COUNT    4  /* a device-held count or length out of range was clamped    */
-#define SGQ_STATUS_TIMEOUT      8  /* a bounded wait inside a GEMV kernel ran out: y is not valid */
+#define SGQ_STATUS_TIMEOUT      8  /* a bounded wait inside a kernel ran out: y (out) is not valid */
 #define SGQ_STATUS_NO_PAGES    16  /* sgq_cache_plan: the free list does not hold enough pages  */
 /* After SGQ_STATUS_TIMEOUT the tensor-core kernel may have freed its tensor
  * memory with MMAs still in flight: treat it as fatal for the results of that
@@ -379,9 +379,8 @@ int sgq_gemv_thresh_noalloc(const void *qweight, const void *sz, int N, int K, i
 
 /*
  * The step around the projections: a paged key/value cache, attention of a
- * step's new tokens over it, and the norms around a block. The pages these
- * kernels' GEMVs come from say nothing of them; they are what a decode or
- * verification step of 1..16 rows (and wider ones) needs next to its GEMVs.
+ * step's new tokens over it, and the norms around a block: what a decode or
+ * verification step needs next to its GEMVs.
  *
  * A cache is num_pages pages of `page` slots; a slot holds one token's keys
  * (values) of every kv head, `dim` elements each. Element e of (page g, slot s
@@ -398,7 +397,7 @@ typedef struct sgq_cache {
     int heads;         /* kv heads                                                    */
     int dim;           /* 64 or 128                                                   */
     long long page_stride, slot_stride, head_stride; /* elements; multiples of 16 bytes,
-                          and at least dim where there is more than one             */
+                          up to 2^38, and at least dim where there is more than one  */
     float k_scale, v_scale; /* 1 for SGQ_TYPE_BF16, finite and > 0 for SGQ_TYPE_E4M3 */
 } sgq_cache;
 
@@ -449,8 +448,8 @@ int sgq_cache_plan(const int32_t *lens, const int32_t *news, int R, int page, in
  *   q, k, v   bf16 rows of T tokens, ld_* elements apart (e.g. the three parts
  *             of one stacked projection's output). q may be NULL (then Hq and
  *             q_out are not used).
- *   n_tokens  optional int32 device scalar (e.g. cu_new + R): rows behind it
- *             are neither read nor written. Outside [0, T]: clamped, flagged
+ *   n_tokens  optional int32 device scalar (e.g. cu_new + R): nothing is
+ *             written for the rows behind it. Outside [0, T]: clamped, flagged
  *             SGQ_STATUS_BAD_COUNT.
  *   rope      optional fp32 [rope_len][dim]: cos of the dim/2 angles of a
  *             position, then sin. NULL: q and k are stored as they are.
@@ -487,9 +486,12 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  *             (normally itself and its ancestors); tokens past 32 * tree_words
  *             are seen by none. NULL: itself and those before it. Every token
  *             sees all lens[r] cached ones.
- *   out       bf16 [T][Hq][dim], rows ld_out apart. lse: optional fp32 [T][Hq].
- *   workspace sgq_tree_attn_workspace_bytes bytes, any content; it holds
- *             nothing between calls. Calls that may overlap must not share one.
+ *   scale     finite (|scale| k_scale <= 1e37), of either sign.
+ *   out       bf16 [T][Hq][dim], rows ld_out apart, not q. lse: optional fp32
+ *             [T][Hq].
+ *   workspace sgq_tree_attn_workspace_bytes bytes for these T, R, Hq, heads and
+ *             dim, any content; it holds nothing between calls. Calls that may
+ *             overlap must not share one.
  * A token that sees no key has out = 0 and lse = -infinity. A key that a token
  * does not see does not touch its output, whatever the slot holds (NaN too).
  * Rows of no request are left as they were. A page outside [0, num_pages) is
@@ -497,9 +499,12 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  * outside the buffers' sizes are clamped and set SGQ_STATUS_BAD_COUNT.
  * Scores, maxima, sums and accumulators are fp32; the weights are rounded to
  * bf16 (fp16 with an SGQ_TYPE_E4M3 cache) for their product with the values.
- * Any T, lengths and shares of Hq / heads; table_ld * page <= 2^30. The grid
- * depends on the arguments alone and nothing is read back: a call can be
- * captured and replayed on other lengths.
+ * With an SGQ_TYPE_E4M3 cache q enters its product as the sum of two 8-bit
+ * parts: each element is off by at most 2^-17 of its row's largest.
+ * Any lengths and shares of Hq / heads, Hq <= 32768, T * Hq < 2^31,
+ * table_ld * page <= 2^30. The grid depends on the arguments alone and nothing
+ * is read back: a call can be captured and replayed on other lengths. The
+ * kernel's waits are bounded by 0.2 s: SGQ_STATUS_TIMEOUT says that one ran out.
  */
 size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D);
 int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,

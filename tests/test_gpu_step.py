@@ -403,6 +403,65 @@ def test_attention_rows_that_see_nothing_and_masked_values_that_are_not_finite()
                 assert (got[1] == 0).all() and (lse[1] == -math.inf).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,n", [(1, 5), (8, 9), (8, 40)])    # up to 32, 128 and more rows
+@pytest.mark.parametrize("lens", [[0, 40], [61, 0], [250, 130]])
+def test_attention_values_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, Hq, n, lens):
+    c = AttnCase(lens, [n, n], Hq, 1, 64, 16, "nhd", dtype, "random", seed=n)
+    w = torch.uint8 if dtype == E4M3 else torch.int16
+    for j in (1, n - 1):            # tokens that see themselves and that no other sees
+        for r in range(2):
+            p = lens[r] + j
+            bad = torch.full((1, 64), math.nan).to(dtype)
+            if dtype == BF16:
+                bad[:, ::2] = -math.inf
+            for x in (c.k, c.v):
+                x.view(w)[int(c.table[r, p // 16]), p % 16] = bad.view(w).to(DEV)
+            for i in range(n):
+                if i != j:
+                    c.tree[c.cu[r] + i, j // 32] &= ~(1 << (j % 32))
+                    c.sees[r][i, p] = False
+    c.run()
+    own = [c.cu[r] + j for r in range(2) for j in (1, n - 1)]
+    assert torch.isnan(c.out[own].float()).any(-1).all()
+    rest = [t for t in range(c.T) if t not in own]
+    for r in range(2):              # without their rows the oracle has nothing that is not finite
+        for j in (1, n - 1):
+            c.sees[r][j] = False
+    ref, rl, mag, dots = so.attention(c.q, c.lens, c.cu, c.keys, c.vals, c.sees, c.scale, c.ks, c.vs, dtype == E4M3)
+    to, tl = so.attention_tolerance(ref, rl, mag, dots, 64, 2.0 ** -11 if dtype == E4M3 else 2.0 ** -8)
+    assert ((c.out.cpu().double() - ref).abs() <= to)[rest].all()
+    fin = torch.isfinite(rl)
+    fin[own] = False
+    assert ((c.lse.cpu().double() - rl).abs() <= tl)[fin].all()
+
+
+@pytest.mark.parametrize("Hq,n,D,page,dtype", [
+    (8, 2, 128, 16, BF16), (8, 2, 64, 24, BF16), (8, 2, 128, 16, E4M3), (8, 2, 64, 24, E4M3), (16, 2, 128, 7, BF16),
+    (32, 10, 128, 16, BF16), (32, 10, 64, 24, E4M3), (32, 40, 128, 16, BF16), (32, 40, 64, 12, E4M3)])
+def test_attention_of_many_tiles_in_a_row(Hq, n, D, page, dtype):
+    # 8 key heads of 25,000 keys in all: every SM goes through its rings several times
+    AttnCase([6000, 300, 7001, 5500, 6200], [n, 1, n, n, n - 1], Hq, 8, D, page, "nhd", dtype, None, seed=n + D).run().check()
+
+
+def test_attention_workspace_of_16_byte_alignment_and_shared_by_two_graphs():
+    cs = [AttnCase([900, 20], [n, 2], 8, 2, 64, 16, seed=n) for n in (3, 40)]
+    need = max(c.ws.numel() for c in cs)
+    ws = torch.empty(need + 4, dtype=torch.int32, device=DEV)[4:]
+    assert ws.data_ptr() % 32 == 16
+    args, graphs = [c.args(workspace=ws) for c in cs], []
+    torch.cuda.synchronize()
+    for a in args:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            sgq.sgq_tree_attn(**a)
+    for g in graphs * 2:            # one after the other on one stream
+        g.replay()
+    torch.cuda.synchronize()
+    for c in cs:
+        c.check()
+
+
 def test_attention_pages_out_of_range_are_masked_and_flagged():
     for dtype in (BF16, E4M3):
         c = AttnCase([100, 70], [3, 2], 4, 2, 64, 16, "nhd", dtype, None, seed=2)

@@ -41,7 +41,7 @@ CACHE_FAULTS = [
     (dict(type=1), -11), (dict(type=7), -11), (dict(dim=96), -2), (dict(dim=256), -2), (dict(heads=0), -2),
     (dict(page=0), -2), (dict(num_pages=0), -2), (dict(k=None), -1), (dict(v=None), -1), (dict(k=(1 << 20) + 2), -4),
     (dict(slot_stride=1028), -4), (dict(head_stride=64), -2), (dict(slot_stride=0), -2), (dict(page_stride=-8), -2),
-    (dict(page_stride=0), -2), (dict(k_scale=0.5), -2), (dict(type=2, k_scale=0.0), -2),
+    (dict(page_stride=0), -2), (dict(page_stride=(1 << 38) + 8), -2), (dict(k_scale=0.5), -2), (dict(type=2, k_scale=0.0), -2),
     (dict(type=2, v_scale=math.nan), -2), (dict(type=2, k_scale=math.inf), -2), (dict(type=2, head_stride=136), -4),
 ]
 
@@ -58,7 +58,8 @@ ATTN_FAULTS = [
     (dict(table_ld=0), -2), (dict(table_ld=1 << 27), -2), (dict(words=0), -2), (dict(q=None), -1), (dict(lens=None), -1),
     (dict(cu=None), -1), (dict(table=None), -1), (dict(out=None), -1), (dict(ws=None), -1), (dict(q=ODD), -4),
     (dict(out=ODD), -4), (dict(ws=ODD), -4), (dict(ld_q=4095), -2), (dict(ld_q=4100), -2), (dict(ld_out=64), -2),
-    (dict(T=1 << 30), -2), (dict(wsb=1 << 20), -6),
+    (dict(T=1 << 30), -2), (dict(wsb=1 << 20), -6), (dict(scale=F(math.nan)), -2), (dict(scale=F(math.inf)), -2),
+    (dict(scale=F(-2e37)), -2),
 ]
 
 
@@ -147,6 +148,14 @@ def test_binding_refuses_types_devices_and_shapes():
     assert (c.struct.page_stride, c.struct.slot_stride, c.struct.head_stride) == (2048, 128, 64)
     with pytest.raises(ValueError, match="current device"):
         c.on(0)
+
+
+def test_cache_of_one_page_head_or_slot_takes_any_stride_there():
+    one = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    k = one.as_strided((1, 2, 1, 64), (7, 64, 3, 1))
+    v = one.as_strided((1, 2, 1, 64), (64, 64, 1, 1))
+    c = sgq.Cache(k, v)
+    assert (c.struct.page_stride, c.struct.slot_stride, c.struct.head_stride) == (64, 64, 64)
 
 
 # ---- the oracle's pins ----
