@@ -130,9 +130,9 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:  # the current stream's handle (building a torch Stream object takes 3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -418,7 +418,7 @@ def sgq_cache_plan(lens, news, R, page, num_pages, table, table_ld, held, held_o
                    free_count, free_count_out, depth, max_tokens, cu_new, slots, pos, req,
                    status=None, stream=None):
     """Block tables, slots and positions of the requests' new tokens, on the GPU."""
-    d = torch.cuda.current_device()
+    d = torch._C._cuda_getDevice()
     _check("sgq_cache_plan", load().sgq_cache_plan(
         _dev("lens", lens, _I32, d), _dev("news", news, _I32, d), R, page, num_pages,
         _dev("table", table, _I32, d), table_ld, _dev("held", held, _I32, d),
@@ -426,19 +426,19 @@ def sgq_cache_plan(lens, news, R, page, num_pages, table, table_ld, held, held_o
         _dev("free_count", free_count, _I32, d), _dev("free_count_out", free_count_out, _I32, d),
         _dev("depth", depth, _I32, d), max_tokens, _dev("cu_new", cu_new, _I32, d),
         _dev("slots", slots, _I64, d), _dev("pos", pos, _I32, d), _dev("req", req, _I32, d),
-        _dev("status", status, _I32, d), _stream(stream)))
+        _dev("status", status, _I32, d), _stream(stream, d)))
 
 
 def sgq_cache_write(q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_len, slots,
                     q_out, ld_qo, cache, status=None, stream=None):
     """Rotate q and k by position; q to q_out, k and v into their slots of ``cache`` (a Cache)."""
-    d = torch.cuda.current_device()
+    d = torch._C._cuda_getDevice()
     _check("sgq_cache_write", load().sgq_cache_write(
         _dev("q", q, _BF16, d), ld_q, _dev("k", k, _BF16, d), ld_k, _dev("v", v, _BF16, d), ld_v,
         T, _dev("n_tokens", n_tokens, _I32, d), Hq, _dev("pos", pos, _I32, d),
         _dev("rope", rope, _F32, d), rope_len, _dev("slots", slots, _I64, d),
         _dev("q_out", q_out, _BF16, d), ld_qo, cache.on(d), _dev("status", status, _I32, d),
-        _stream(stream)))
+        _stream(stream, d)))
 
 
 def sgq_tree_attn_workspace_bytes(T: int, R: int, Hq: int, Hkv: int, D: int) -> int:
@@ -448,21 +448,21 @@ def sgq_tree_attn_workspace_bytes(T: int, R: int, Hq: int, Hkv: int, D: int) -> 
 def sgq_tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
                   scale, out, ld_out, lse, workspace, status=None, stream=None):
     """Attention of each request's new tokens over its pages of ``cache`` (a Cache)."""
-    d = torch.cuda.current_device()
+    d = torch._C._cuda_getDevice()
     _check("sgq_tree_attn", load().sgq_tree_attn(
         _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _I32, d),
         _dev("cu_new", cu_new, _I32, d), _dev("table", table, _I32, d), table_ld, cache.on(d),
         _dev("tree", tree, _I32, d), tree_words, scale, _dev("out", out, _BF16, d), ld_out,
         _dev("lse", lse, _F32, d), _dev("workspace", workspace, _I32, d),
         0 if workspace is None else workspace.nbytes,
-        _dev("status", status, _I32, d), _stream(stream)))
+        _dev("status", status, _I32, d), _stream(stream, d)))
 
 
 def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_out, ld_ro,
                       w_pre, w_offset, x, ld_x, B, H, eps, stream=None):
     """The norms around a block with its gate and scaled residual; the element
     types of the C entry point (a_type, r_type, w_type) are the tensors' own."""
-    d = torch.cuda.current_device()
+    d = torch._C._cuda_getDevice()
     w = w_pre if w_pre is not None else w_post if w_post is not None else gate
     at, rt = None if a is None else a.dtype, None if resid is None else resid.dtype
     wt = None if w is None else w.dtype
@@ -472,7 +472,7 @@ def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_
         _dev("resid", resid, rt, d), ld_r, SGQ_TYPE_F32 if resid is None else _float_type("resid", resid),
         _dev("resid_out", resid_out, rt, d), ld_ro, _dev("w_pre", w_pre, wt, d),
         SGQ_TYPE_F32 if w is None else _float_type("w_pre, w_post and gate", w), w_offset,
-        _dev("x", x, _BF16, d), ld_x, B, H, eps, _stream(stream)))
+        _dev("x", x, _BF16, d), ld_x, B, H, eps, _stream(stream, d)))
 
 
 # --------------------------------------------------------------------------
