@@ -1,5 +1,7 @@
 """activation_sparse_quantized_b200 -- activation-sparse GEMV over group-wise
-int4 weights, as hand-written CUDA for B200 (sm_100a) behind a C ABI.
+int4 weights and the rest of a decode step around it (paged cache, tree
+attention, residual norms), as hand-written CUDA for B200 (sm_100a) behind a C
+ABI.
 
 ``sgq``        the thin ctypes binding to ``libsgq.so`` (same names as the C ABI)
 ``workloads``  seeded synthetic inputs (shapes and distributions only)

@@ -47,6 +47,20 @@
 // side in shared memory, where the product reads it (its rows from 32 on are
 // whatever lies there, and so are those of O).
 //
+// What bounds it: with few rows and 16-bit keys memory (24 requests of 16000 keys
+// and more, 32 query and 8 key heads of 128: 246 to 253 us, 6.2 to 6.4 TB/s), with
+// 8-bit ones the products' reads of shared memory and the hand-offs; with 512 rows
+// a request the chain of a tile, scores, exponentials, products (12 requests of up
+// to 16384 keys, 64 / 8 heads of 128: 164 us, 618 TFLOP/s). Slower there: scores in
+// halves of 64 keys, one with the softmax while the next are computed (171); 64
+// scores in registers at a time (177), and the other warps' registers for them
+// (187). Slower with few rows: scores two tiles ahead (75 us against 54 on 24
+// requests of up to 16111 keys), for which the ring holds too little.
+//
+// The copies' ring tells a slot's phases by their parity alone. That holds as long
+// as scores are one tile ahead of the products with the values: in a ring of an odd
+// number of slots the values two turns back are then used up before the keys between.
+//
 // Every wait on a barrier is bounded by 0.2 s; one that runs out sets
 // SGQ_STATUS_TIMEOUT, the thread waits for no data any more and the kernel runs
 // to its end. The segments are passed on all the same (those waits, bounded by
