@@ -2,7 +2,10 @@
 (step_oracle): cache plan, cache store, tree attention, residual norm, and a
 run of them together with the GEMVs. Tolerances are derived in step_oracle."""
 import math
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -442,6 +445,42 @@ def test_attention_values_that_are_not_finite_reach_only_the_rows_that_see_them(
 def test_attention_of_many_tiles_in_a_row(Hq, n, D, page, dtype):
     # 8 key heads of 25,000 keys in all: every SM goes through its rings several times
     AttnCase([6000, 300, 7001, 5500, 6200], [n, 1, n, n, n - 1], Hq, 8, D, page, "nhd", dtype, None, seed=n + D).run().check()
+
+
+def test_attention_of_as_many_requests_as_there_may_be_and_of_many_heads():
+    rng = random.Random(8)
+    R = sgq.SGQ_MAX_REQUESTS
+    AttnCase([rng.randint(0, 9) for _ in range(R)], [rng.randint(0, 1) for _ in range(R)], 2, 1, 64, 4, seed=8).run().check()
+    AttnCase([33, 2], [2, 1], 128, 64, 64, 8, seed=9).run().check()
+    AttnCase([150], [2], 300, 1, 128, 16, seed=10).run().check()    # one key head for 300
+
+
+FIRST_CALL = '''
+import torch
+import __graft_entry__ as g
+from activation_sparse_quantized_b200 import sgq
+torch.cuda.set_device(0)
+launched = []
+real = {n: getattr(sgq, n) for n in ("sgq_cache_plan", "sgq_cache_write", "sgq_tree_attn", "sgq_residual_norm")}
+def captured(name):
+    def call(*a):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            real[name](*a)
+        graph.replay()
+        launched.append((name, graph))
+    return call
+for n in real:
+    setattr(sgq, n, captured(n))
+g.smoke_step("cuda:0")
+assert len(launched) == 4
+'''
+
+
+def test_first_call_of_a_process_may_be_captured():
+    subprocess.run([sys.executable, "-c", FIRST_CALL], check=True, timeout=120,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 def test_attention_workspace_of_16_byte_alignment_and_shared_by_two_graphs():
