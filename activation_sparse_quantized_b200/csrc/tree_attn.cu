@@ -662,8 +662,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 cp_async_arrive(bQ);
                 free_ph ^= 1;
             } else {
+                // rows behind the tile's own are left as they lie: nothing of theirs is written
+                const int used = n * G - g0;
 #pragma unroll 1
-                for (int k0 = 0; k0 < ALL; k0 += N) {
+                for (int k0 = 0; k0 < ALL && k0 * QT / CH < used; k0 += N) {
                     uint4 v[N];
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
@@ -679,6 +681,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
+                        if ((k0 + k) * QT / CH >= used)
+                            break;
                         const int idx = ct + (k0 + k) * QT, qr = idx / CH, c = idx % CH;
                         uint8_t *dst = smem + (C::TWO ? (qr >> 7) * C::Q1 : 0);
                         const int r = C::TWO ? qr & 127 : qr;
