@@ -923,6 +923,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
                                 tmem_st16(tO + c, o);
                             }
+                            tmem_st_wait(); // the product that bP lets in adds to what is stored here
                         }
                     }
                     return m == -INFINITY ? 0.0f : m; // nothing seen yet

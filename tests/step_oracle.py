@@ -151,3 +151,34 @@ def norm(a, w_post, gate, scale, resid, w_pre, w_offset, eps):
         f = (w_offset + w_pre.double()) / torch.sqrt((r * r).mean(-1, keepdim=True) + eps)
         x = r * f
     return r, x, tol, f
+
+
+def attention_by_head(q, cu, keys, vals, sees, scale, k_scale=1.0, v_scale=1.0, eight=False):
+    """What ``attention`` returns, with a key head's rows taken together (long contexts,
+    many rows)."""
+    T, Hq, D = q.shape
+    out = torch.zeros(T, Hq, D, dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    lse = torch.full((T, Hq), -math.inf, dtype=torch.float64)
+    dots = torch.zeros(T, Hq, dtype=torch.float64)
+    for r in range(len(keys)):
+        t0, n = cu[r], cu[r + 1] - cu[r]
+        G = Hq // keys[r].shape[1]
+        for h in range(keys[r].shape[1]):
+            rows = slice(t0, t0 + n), slice(h * G, (h + 1) * G)
+            x, k, v = q[rows].double(), keys[r][:, h], vals[r][:, h]
+            hidden = ~sees[r][:, None, :]
+            s = torch.einsum("ngd,ld->ngl", x, k) * (scale * k_scale)
+            s = s.masked_fill(hidden, -math.inf)
+            top = s.amax(-1, keepdim=True)
+            w = (s - top.clamp(min=-1e300)).exp()
+            total = w.sum(-1, keepdim=True)
+            w = w / total.clamp(min=1e-300)
+            out[rows] = torch.einsum("ngl,ld->ngd", w, v) * v_scale
+            mag[rows] = torch.einsum("ngl,ld->ngd", w, v.abs()) * v_scale
+            lse[rows] = (top + total.log())[..., 0]
+            d = torch.einsum("ngd,ld->ngl", x.abs(), k.abs())
+            if eight:
+                d = d + k.abs().sum(-1) * x.abs().amax(-1, keepdim=True) * (2.0 ** -17 / ((D + 8) * U))
+            dots[rows] = d.masked_fill(hidden, 0.0).amax(-1) * abs(scale * k_scale)
+    return out, lse, mag, dots

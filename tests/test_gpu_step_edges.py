@@ -1,0 +1,84 @@
+"""The step entry points where sums, references and hand-offs are stretched:
+maxima that grow along a run, weights far below the largest, scores and queries
+at the ends of their types, many tokens, long runs, waits that run out. Against
+the fp64 definitions (step_oracle), as in test_gpu_step."""
+import math
+
+import pytest
+import torch
+
+import step_oracle as so
+from activation_sparse_quantized_b200 import build, sgq
+from test_gpu_step import AttnCase
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    torch.cuda.set_device(0)
+    return sgq.load()
+
+
+class Attn(AttnCase):
+    """An AttnCase whose keys and values can be put in place, checked a key head at a time."""
+
+    def put(self, r, keys=None, vals=None):
+        """Keys, values [L, Hkv, D] of request r, rounded to the cache's type."""
+        w = torch.uint8 if self.k.dtype == E4M3 else torch.int16
+        p = torch.arange(self.lens[r] + self.news[r])
+        at = self.table[r].long()[p // self.page].to(DEV), (p % self.page).to(DEV)
+        for x, y, to in ((self.k, keys, self.keys), (self.v, vals, self.vals)):
+            if y is not None:
+                y = y.to(self.k.dtype)
+                x.view(w)[at] = y.view(w).to(DEV)
+                to[r] = y.to(F32).double()
+
+    def expected(self):
+        f8 = self.k.dtype == E4M3
+        out, lse, mag, dots = so.attention_by_head(self.q, self.cu, self.keys, self.vals, self.sees, self.scale, self.ks, self.vs, f8)
+        return out, lse, *so.attention_tolerance(out, lse, mag, dots, self.D, 2.0 ** -11 if f8 else 2.0 ** -8)
+
+    def check(self, status=0, rows=None):
+        assert self.status.item() == status
+        out, lse, to, tl = self.expected()
+        rows = list(range(self.cu[-1])) if rows is None else rows
+        d = ((self.out.cpu().double() - out).abs() / to)[rows]
+        assert (d <= 1).all(), float(d.nan_to_num(math.inf).max())
+        assert ((self.lse.cpu().double() - lse).abs() <= tl)[rows].all()
+        n = self.cu[-1]
+        assert (self.out[n:] == 9.0).all() and (self.lse[n:] == 9.0).all()
+
+
+# ---- maxima that grow along a run ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,n", [(16, 2), (32, 20), (32, 40)])   # tiles of 32, 128 and 256 rows
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attention_maxima_that_outgrow_their_reference(dtype, D, Hq, n, sign):
+    # Eight key heads of 20,000 keys are eight tiles and more in a row on every SM. The
+    # scores climb by 100 binary orders in 1100 keys and fall back, at another pace and
+    # from another place for each row and head, so that what is summed so far is scaled
+    # down many times over, and the top of every climb counts in the result.
+    L, Hkv = 20000, 8
+    c = Attn([L], [n], Hq, Hkv, D, 32, "nhd", dtype, None, seed=n + D)
+    g = torch.Generator().manual_seed(n)
+    ones = torch.ones(D)
+    climb = ((torch.arange(L + n)[:, None] + 137 * torch.arange(Hkv)) % 1100) / 1100 * 100
+    unit = math.log(2) / (D * c.scale * c.ks)              # a key of this, times ones, is one binary order
+    c.put(0, (climb * unit)[..., None] * ones + 0.05 * torch.randn(L + n, Hkv, D, generator=g))
+    pace = 0.3 + torch.rand(n, Hq, 1, generator=g)
+    c.q = (sign * pace * ones).to(BF16)
+    c.scale *= sign
+    c.run().check()
+    first = c.out.clone(), c.lse.clone()
+    for _ in range(4):
+        c.run()
+        assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
