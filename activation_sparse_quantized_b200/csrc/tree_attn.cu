@@ -864,7 +864,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             rq.len = sg.len;
             const uint64_t first = takes && sg.first_tail < sg.nt ? tree_bits(p, rq, tok_i) : 0;
             float factor = fmaxf(base_factor, 1e-37f); // a scale of zero: all scores alike
-            float m = -INFINITY, l = 0.0f;             // reference (base 2), sum
+            // the reference, as a score and in base 2, and the sum
+            float ms = -INFINITY, m = -INFINITY, l = 0.0f;
 
 #pragma unroll 1
             for (int t = t0; t < sg.nt; t += dt) {
@@ -908,10 +909,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 // The reference moves for the first keys seen, and when outgrown;
                 // O (by the warp that has its lanes) and l with it.
                 auto refer = [&](float top) {
-                    const bool grow = top > m + kGrowth;
+                    const bool grow = (top - ms) * factor > kGrowth;
                     if (__any_sync(~0u, grow)) {
-                        const float corr = grow ? exp2_fast(m - top) : 1.0f;
-                        m = grow ? top : m;
+                        const float corr = grow ? exp2_fast((ms - top) * factor) : 1.0f;
+                        ms = grow ? top : ms;
+                        m = grow ? top * factor : m;
                         l *= corr;
                         if (t >= dt && quad == 0) { // this group's last product is done: S was issued after it
 #pragma unroll 1
@@ -933,11 +935,17 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 // small ones, 2^-25); their sum l is of the unrounded ones.
                 // (A third of the exponentials by polynomial on the FMA pipe did
                 // not change 12 wide trees' 175 us, half of them made it 184.)
+                // The reference is taken off as a score, before the factor: in base 2 it is
+                // rounded, and from 2^28 on by more than the weights' type can take. (That is an
+                // addition per pair of scores: 191.5 us against 188.6 on 12 wide trees, 77.1
+                // against 76.0 on 11 requests of 8-bit keys; a branch to it for large references
+                // costs those 188.8 and 81.) A row whose reference leaves fp32 in base 2 is NaN.
                 auto weigh = [&](const uint32_t *s, float ref, uint32_t *w, float2 *sum) {
+                    const float score = ms == -INFINITY ? 0.0f : ms, zero = ref * 0.0f;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                         make_float2(factor, factor), make_float2(-ref, -ref));
+                        float2 x = add2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(-score, -score));
+                        x = ffma2(x, make_float2(factor, factor), make_float2(zero, zero));
                         x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
                         w[e / 2] = pack2<C::F8>(x.x, x.y);
@@ -959,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
 #pragma unroll
                     for (int c = 1; c < 4; ++c)
                         top = fmaxf(top, s_mx[2 * grp + s_ph][c][lane]);
-                    const float ref = refer(top * factor);
+                    const float ref = refer(top);
                     weigh(s, ref, w, sum);
                     uint8_t *dst = smem + (sP - sQ) + grp * C::P1 + (quad >> 1) * C::ROWS * 128 + row * 128;
 #pragma unroll
@@ -982,7 +990,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         highest(s, mx);
                     }
                     tmem_st_wait();
-                    const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor);
+                    const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(tS + 32 * c, s);

@@ -82,3 +82,29 @@ def test_attention_maxima_that_outgrow_their_reference(dtype, D, Hq, n, sign):
     for _ in range(4):
         c.run()
         assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
+# ---- scores of any size ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,n", [(4, 2), (8, 9), (8, 40)])
+@pytest.mark.parametrize("power", [12, 26, 34, 60, 110])
+def test_attention_scores_far_beyond_the_exponents_range(dtype, Hq, n, power):
+    # Small whole numbers times powers of two: every product and sum is exact, scores
+    # differ by 2^power times a whole number over D or not at all, and a row's result is
+    # the mean of the values at its highest score. (D = 64: scale 1/8 is exact too.)
+    g = torch.Generator().manual_seed(power + n)
+    c = Attn([1500, 200], [n, n], Hq, 1, 64, 16, "nhd", dtype, None, seed=n)
+    for r in range(2):
+        c.put(r, torch.randint(-3, 4, (c.lens[r] + n, 1, 64), generator=g).float())
+    c.q = (torch.randint(-3, 4, (2 * n, Hq, 64), generator=g) * 2.0 ** power).to(BF16)
+    c.ks = 1.0
+    c.run()
+    assert c.status.item() == 0
+    out, lse, _, _ = so.attention_by_head(c.q, c.cu, c.keys, c.vals, c.sees, c.scale, c.ks, c.vs)
+    got = c.out.cpu().double()
+    # a weight's and the result's rounding, and the sums', as in attention_tolerance without a score's error
+    most = max(float(v.abs().max()) for v in c.vals) * c.vs
+    to = ((2.0 ** -11 if dtype == E4M3 else 2.0 ** -8) + 2.0 ** -14) * most
+    assert ((got - out).abs() <= to + 2.0 ** -8 * (out.abs() + to)).all()
+    assert ((c.lse.cpu().double() - lse).abs() <= 2.0 ** -20 + 8 * so.U * lse.abs()).all()
