@@ -82,6 +82,9 @@ constexpr int kGroup = 128; // threads of a softmax group
 constexpr int kSoftWarps = 8, kKeys = 8, kValues = 9, kIssuer = 10, kQ = 11; // warps
 constexpr uint32_t kColO = 256; // tensor-memory columns: S0, S1, the groups' O
 constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its reference
+// fp16 weights (8-bit caches) are 2^7 times the bf16 ones: up to 2^15 of fp16's 2^16, and so
+// with all the room below that there is (the sums l carry the same factor).
+constexpr float kLift16 = 7.0f;
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
 constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
@@ -97,6 +100,7 @@ struct Cfg {
     static constexpr int COPIES = 128 / ROWS;                 // of the rows, in Q
     static constexpr int SUB = kTile * 128;                   // 128 rows x 128 bytes, swizzled
     static constexpr int NSUB = D / 64;
+    static constexpr float LIFT = F8 ? kLift16 : 0.0f;
     static constexpr int SLOT = NSUB * SUB;                   // 128 keys (or values), 16 bits
     static constexpr int Q1 = F8 ? 2 * SUB : SLOT, Q = TWO ? 2 * Q1 : Q1; // 128 rows of q; all of them
     static constexpr int P1 = FEW ? ROWS * 256 : 0, P = 2 * P1; // P of a group in shared memory
@@ -931,8 +935,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     return m == -INFINITY ? 0.0f : m; // nothing seen yet
                 };
                 // The weights are rounded to the values' type for the product
-                // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, the
-                // small ones, 2^-25); their sum l is of the unrounded ones.
+                // (bf16: off by at most 2^-8 of each, fp16: 2^-11 or, those below
+                // 2^-14, 2^-25, which is 2^-32 of the row's largest at most); their
+                // sum l is of the unrounded ones.
                 // (A third of the exponentials by polynomial on the FMA pipe did
                 // not change 12 wide trees' 175 us, half of them made it 184.)
                 // The reference is taken off as a score, before the factor: in base 2 it is
@@ -941,11 +946,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 // against 76.0 on 11 requests of 8-bit keys; a branch to it for large references
                 // costs those 188.8 and 81.) A row whose reference leaves fp32 in base 2 is NaN.
                 auto weigh = [&](const uint32_t *s, float ref, uint32_t *w, float2 *sum) {
-                    const float score = ms == -INFINITY ? 0.0f : ms, zero = ref * 0.0f;
+                    const float score = ms == -INFINITY ? 0.0f : ms, lift = ref * 0.0f + C::LIFT;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 x = add2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(-score, -score));
-                        x = ffma2(x, make_float2(factor, factor), make_float2(zero, zero));
+                        x = ffma2(x, make_float2(factor, factor), make_float2(lift, lift));
                         x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
                         w[e / 2] = pack2<C::F8>(x.x, x.y);
@@ -1093,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                             part[MT * D + trow] = top;
                             part[MT * D + MT + trow] = l;
                         } else if (p.lse) {
-                            p.lse[tk * p.Hq + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+                            p.lse[tk * p.Hq + hq] = l == 0.0f ? -INFINITY : (top + (log2f(l) - C::LIFT)) * kLn2;
                         }
                     }
                     if (sg.whole) // the sum's inverse and the values' scale, on the way
@@ -1340,14 +1345,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) join_kernel(const AttnProb
         if (k < mine && row < rows && warp % wpu == 0) {
             const int g = sp.rt * MT + row, ti = g / G, hq = sp.h * G + g - ti * G;
             const long long t = sp.tok + ti;
-            const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l;
+            const float inv = l == 0.0f ? 0.0f : p.cache.v_scale / l, lift = p.cache.type == SGQ_TYPE_E4M3 ? kLift16 : 0.0f;
             uint16_t *out = p.out + t * p.ld_out + (long long)hq * D + 4 * c4;
 #pragma unroll
             for (int x = 0; x < VEC; ++x)
                 *reinterpret_cast<uint2 *>(out + 16 * x) =
                     make_uint2(pack2<false>(o[x].x * inv, o[x].y * inv), pack2<false>(o[x].z * inv, o[x].w * inv));
             if (p.lse && c4 == 0)
-                p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+                p.lse[t * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + (log2f(l) - lift)) * kLn2;
         }
     }
 }

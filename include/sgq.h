@@ -498,7 +498,8 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  * skipped, its keys unseen, and sets SGQ_STATUS_BAD_INDEX; lengths and rows
  * outside the buffers' sizes are clamped and set SGQ_STATUS_BAD_COUNT.
  * Scores, maxima, sums and accumulators are fp32; the weights are rounded to
- * bf16 (fp16 with an SGQ_TYPE_E4M3 cache) for their product with the values.
+ * bf16 for their product with the values, with an SGQ_TYPE_E4M3 cache to fp16:
+ * those below 2^-21 of their row's largest are then off by up to 2^-32 of it.
  * With an SGQ_TYPE_E4M3 cache q enters its product as the sum of two 8-bit
  * parts: each element is off by at most 2^-17 of its row's largest.
  * Any lengths and shares of Hq / heads, Hq <= 32768, T * Hq < 2^31,

@@ -108,3 +108,43 @@ def test_attention_scores_far_beyond_the_exponents_range(dtype, Hq, n, power):
     to = ((2.0 ** -11 if dtype == E4M3 else 2.0 ** -8) + 2.0 ** -14) * most
     assert ((got - out).abs() <= to + 2.0 ** -8 * (out.abs() + to)).all()
     assert ((c.lse.cpu().double() - lse).abs() <= 2.0 ** -20 + 8 * so.U * lse.abs()).all()
+
+
+# ---- weights far below the largest ----
+
+def share(c, R):
+    """The one request of c, of one new token, R times over the same pages, with a q each."""
+    c.lens, c.news, c.cu, c.T = c.lens * R, c.news * R, list(range(R + 1)), R
+    c.table = c.table.expand(R, -1).contiguous()
+    c.keys, c.vals, c.sees = c.keys * R, c.vals * R, c.sees * R
+    c.ws = sgq.alloc_tree_attn_workspace(R, R, c.Hq, c.Hkv, c.D)
+    c.out = torch.full((R, c.Hq, c.D), 9.0, dtype=BF16, device=DEV)
+    c.lse = torch.full((R, c.Hq), 9.0, device=DEV)
+    return c
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_a_long_tail_below_one_key_whose_value_is_zero(dtype, D):
+    # One key, the first, 10 to 20 nats above 60,000 others: its value is zero, so the
+    # result is the others'. Two requests a SM, so that most are not cut into parts
+    # (each part has a reference of its own).
+    L, R = 60000, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(D)
+    c = Attn([L], [1], 1, 1, D, 64, "nhd", dtype, None, seed=D)
+    keys = -1 + 0.0625 * torch.randint(0, 2, (L + 1, 1, D), generator=g)
+    vals = 1 + 0.25 * torch.randint(-2, 3, (L + 1, 1, D), generator=g)
+    keys[0], vals[0] = 1.0, 0.0
+    c.put(0, keys, vals)
+    c = share(c, R)
+    nats = 10 + 10 * torch.arange(R) / (R - 1)                     # the distance to the lowest key
+    c.q = (nats / (2 * D * c.scale * c.ks))[:, None, None].expand(R, 1, D).to(BF16)
+    c.run()
+    assert c.status.item() == 0
+    out, lse, to, tl = c.expected()
+    # The largest weight is 2^7 at least and one below 2^-14 is off by at most 2^-25
+    # (fp16's steps), so each of the keys' weights by 2^-32 of the largest.
+    low = 1.5 * c.vs * L * 2.0 ** -32 if dtype == E4M3 else 0.0
+    assert ((c.out.cpu().double() - out).abs() <= to + low * (1 + 2.0 ** -8)).all()
+    assert ((c.lse.cpu().double() - lse).abs() <= tl).all()
+    assert low < 0.2 * out.abs().min()                             # the bound says something of every row
