@@ -704,7 +704,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
                             // both the power and its inverse are normal fp32 numbers
                             const int up = min(max(7 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
-                            const float mul = pow2f(up);
+                            // (an infinity would be saturated: such a row is made NaN)
+                            const float mul = mx < INFINITY ? pow2f(up) : NAN;
                             uint32_t part[2][2];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {

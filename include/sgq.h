@@ -492,7 +492,10 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  *   workspace sgq_tree_attn_workspace_bytes bytes for these T, R, Hq, heads and
  *             dim, any content; it holds nothing between calls. Calls that may
  *             overlap must not share one.
- * A token that sees no key has out = 0 and lse = -infinity. A key that a token
+ * A token that sees no key, or none with a score above -infinity, has out = 0
+ * and lse = -infinity. Of a row of q with an infinity or NaN out is NaN with an
+ * SGQ_TYPE_E4M3 cache, and what its scores make it with a bf16 one; other rows
+ * are not touched by it. A key that a token
  * does not see does not touch its output, whatever the slot holds (NaN too).
  * Rows of no request are left as they were. A page outside [0, num_pages) is
  * skipped, its keys unseen, and sets SGQ_STATUS_BAD_INDEX; lengths and rows

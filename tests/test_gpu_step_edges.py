@@ -148,3 +148,23 @@ def test_attention_a_long_tail_below_one_key_whose_value_is_zero(dtype, D):
     assert ((c.out.cpu().double() - out).abs() <= to + low * (1 + 2.0 ** -8)).all()
     assert ((c.lse.cpu().double() - lse).abs() <= tl).all()
     assert low < 0.2 * out.abs().min()                             # the bound says something of every row
+
+
+# ---- a q that is not finite ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,n", [(4, 3), (8, 9), (8, 40)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_attention_rows_of_q_that_are_not_finite(dtype, Hq, n, bad):
+    c = Attn([1000, 70], [n, n], Hq, 1, 64, 16, "nhd", dtype, "random", seed=n)
+    rows = [0, n - 1, n + 1]
+    keys = [k.clone() for k in c.keys]
+    for r in range(2):              # one channel's keys are small: products of 448 with them do not overflow
+        keys[r][:, :, 5] *= 0.0625
+        c.put(r, keys[r])
+    for t in rows:
+        c.q[t, :, 5] = bad
+    c.run()
+    assert torch.isnan(c.out[rows].float()).all() and not torch.isfinite(c.lse[rows]).any()
+    c.q[rows] = 0                   # the oracle needs numbers there
+    c.check(rows=[t for t in range(c.cu[-1]) if t not in rows])
