@@ -60,6 +60,57 @@ int check_cache(const sgq_cache *c)
     return SGQ_OK;
 }
 
+int tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,
+              const int32_t *cu_new, const int32_t *table, int table_ld,
+              const sgq_cache *cache_host, const uint32_t *tree, int tree_words,
+              float scale, void *out, long long ld_out, float *lse, void *workspace,
+              size_t ws_bytes, int32_t *status, void *stream, int withhold)
+{
+    int rc = check_cache(cache_host);
+    if (rc)
+        return rc;
+    if (R < 1 || R > SGQ_MAX_REQUESTS)
+        return SGQ_ERR_BATCH;
+    const long long D = cache_host->dim, Hkv = cache_host->heads;
+    if (T < 1 || Hq < Hkv || Hq % Hkv != 0 || table_ld < 1 ||
+        (long long)table_ld * cache_host->page > (1ll << 30) ||
+        Hq > 32768 || (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))) ||
+        !(fabsf(scale) * cache_host->k_scale <= 1e37f)) // (not a number: refused)
+        return SGQ_ERR_SHAPE;
+    if (!q || !lens || !cu_new || !table || !out || !workspace)
+        return SGQ_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+        return SGQ_ERR_ALIGN;
+    if (!stride_ok(ld_q, Hq * D, 2) || !stride_ok(ld_out, Hq * D, 2))
+        return SGQ_ERR_SHAPE;
+    if (ws_bytes < sgq::attn_workspace_bytes(T, R, Hq, (int)Hkv, (int)D))
+        return SGQ_ERR_WORKSPACE;
+    const int sms = sgq::current_device_sms();
+    if (sms < 0)
+        return sms;
+    sgq::AttnProblem p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.lens = lens;
+    p.cu_new = cu_new;
+    p.table = table;
+    p.tree = tree;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.workspace = workspace;
+    p.status = status;
+    p.ld_q = ld_q;
+    p.ld_out = ld_out;
+    p.T = T;
+    p.R = R;
+    p.Hq = Hq;
+    p.table_ld = table_ld;
+    p.tree_words = tree_words;
+    p.scale = scale;
+    p.cache = *cache_host;
+    p.debug_withhold_scores = withhold;
+    return finish(sgq::launch_attn(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
 } // namespace
 
 extern "C" {
@@ -164,48 +215,18 @@ int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int
                   float scale, void *out, long long ld_out, float *lse, void *workspace,
                   size_t ws_bytes, int32_t *status, void *stream)
 {
-    int rc = check_cache(cache_host);
-    if (rc)
-        return rc;
-    if (R < 1 || R > SGQ_MAX_REQUESTS)
-        return SGQ_ERR_BATCH;
-    const long long D = cache_host->dim, Hkv = cache_host->heads;
-    if (T < 1 || Hq < Hkv || Hq % Hkv != 0 || table_ld < 1 ||
-        (long long)table_ld * cache_host->page > (1ll << 30) ||
-        Hq > 32768 || (long long)T * Hq > 0x7fffffffll || (tree && (tree_words < 1 || tree_words > (1 << 25))) ||
-        !(fabsf(scale) * cache_host->k_scale <= 1e37f)) // (not a number: refused)
-        return SGQ_ERR_SHAPE;
-    if (!q || !lens || !cu_new || !table || !out || !workspace)
-        return SGQ_ERR_NULL;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
-        return SGQ_ERR_ALIGN;
-    if (!stride_ok(ld_q, Hq * D, 2) || !stride_ok(ld_out, Hq * D, 2))
-        return SGQ_ERR_SHAPE;
-    if (ws_bytes < sgq::attn_workspace_bytes(T, R, Hq, (int)Hkv, (int)D))
-        return SGQ_ERR_WORKSPACE;
-    const int sms = sgq::current_device_sms();
-    if (sms < 0)
-        return sms;
-    sgq::AttnProblem p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.lens = lens;
-    p.cu_new = cu_new;
-    p.table = table;
-    p.tree = tree;
-    p.out = static_cast<uint16_t *>(out);
-    p.lse = lse;
-    p.workspace = workspace;
-    p.status = status;
-    p.ld_q = ld_q;
-    p.ld_out = ld_out;
-    p.T = T;
-    p.R = R;
-    p.Hq = Hq;
-    p.table_ld = table_ld;
-    p.tree_words = tree_words;
-    p.scale = scale;
-    p.cache = *cache_host;
-    return finish(sgq::launch_attn(p, sms, static_cast<cudaStream_t>(stream)));
+    return tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache_host, tree, tree_words, scale, out, ld_out, lse,
+                     workspace, ws_bytes, status, stream, 0);
+}
+
+int sgq_debug_tree_attn_withhold(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,
+                                 const int32_t *cu_new, const int32_t *table, int table_ld,
+                                 const sgq_cache *cache_host, const uint32_t *tree, int tree_words,
+                                 float scale, void *out, long long ld_out, float *lse, void *workspace,
+                                 size_t ws_bytes, int32_t *status, void *stream)
+{
+    return tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache_host, tree, tree_words, scale, out, ld_out, lse,
+                     workspace, ws_bytes, status, stream, 1);
 }
 
 int sgq_residual_norm(const void *a, long long ld_a, int a_type, const void *w_post,

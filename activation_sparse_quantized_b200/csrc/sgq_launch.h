@@ -125,6 +125,9 @@ struct AttnProblem {
     int T, R, Hq, table_ld, tree_words;
     float scale;
     sgq_cache cache;
+    // test hook: withhold the commits that pass scores on, so that the kernel's
+    // waits run out
+    int debug_withhold_scores;
 };
 
 cudaError_t launch_norm(const NormProblem &p, int num_sms, cudaStream_t stream);

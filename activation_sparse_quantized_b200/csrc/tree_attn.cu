@@ -61,11 +61,14 @@
 // as scores are one tile ahead of the products with the values: in a ring of an odd
 // number of slots the values two turns back are then used up before the keys between.
 //
-// Every wait on a barrier is bounded by 0.2 s; one that runs out sets
-// SGQ_STATUS_TIMEOUT, the thread waits for no data any more and the kernel runs
-// to its end. The segments are passed on all the same (those waits, bounded by
-// 2 s, outlast the others), so the warps of a group still meet at their
-// barriers.
+// Every wait for another warp's work is bounded by 0.2 s, for a segment and for its
+// slot by 2 s; one that runs out sets SGQ_STATUS_TIMEOUT, its warp waits for no data any
+// more and the kernel comes to its end. The warps of a group also meet at barriers of
+// their own, which have no limit: they come to the same ones as long as they work on the
+// same segments, and they do whatever runs out, since the warp that passes segments on
+// stops for good kPassClocks after the last one, well before any other has waited for
+// 2 s (at 250 MHz and more). A segment's slot may then be written before every warp has
+// read it, so what they read there is kept in bounds field by field.
 #include "step_launch.cuh"
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
@@ -89,6 +92,7 @@ constexpr int kRing = 8;        // segments, and tail tiles, that are known to m
 constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
 constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 400000000ull;
+constexpr long long kPassClocks = 500000000; // see the segments' hand-over
 
 template <int D_, int KV, int MT_>
 struct Cfg {
@@ -109,7 +113,7 @@ struct Cfg {
     static constexpr int NV = F8 ? 2 : 0;                     // fp16 values
     static constexpr int ROWB = F8 ? D : 2 * D, CPR = ROWB / 16; // bytes, 16-byte chunks of a key
     static constexpr int OUT1 = 32 * 64, OUT = MT == 128 ? 8 * OUT1 : 0; // 16 columns of a warp's rows, for the other group
-    static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 3;
+    static constexpr int BARS = 2 * SLOTS + 2 * NV + 6 + 3 * kRing + 4;
     static constexpr int SMEM = 1024 + Q + P + KV_BYTES + NV * SLOT + OUT + BARS * 8;
     static_assert(SMEM <= 227 * 1024 - 8192, "room for the static arrays");
     // copies run ahead of the softmax by the ring's tiles, 8-bit ones by NV more and the
@@ -117,7 +121,8 @@ struct Cfg {
     static_assert(SLOTS / 2 + NV + 2 <= kTiles && (F8 ? NV + 1 : SLOTS / 2 + 1) <= kRing, "ring entries");
 };
 
-// What a CTA's warps need of a segment (nt = 0: the run has ended).
+// What a CTA's warps need of a segment (nt = 0: the run has ended). The softmax's warps
+// keep its slot; the others have read it by then, or a wait has run out.
 struct Seg {
     int nt, r;                  // tiles, request
     int tok, n, len;            // the request's first row, new tokens, cached ones
@@ -146,6 +151,19 @@ template <int N>
 __device__ __forceinline__ void named_sync(int bar)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
+}
+
+// named_sync, and whether any of its threads has v != 0.
+template <int N>
+__device__ __forceinline__ bool named_or(int bar, uint32_t v)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(v), "r"(bar), "n"(N)
+                 : "memory");
+    return any;
 }
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
@@ -182,13 +200,14 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     __shared__ float s_f[C::F8 ? 4 : 1][C::F8 ? MT : 1]; // q's powers of two, by segment
     __shared__ uint32_t s_bad[kTiles][4];                // keys without a page, bit by key, by tile
     __shared__ uint32_t s_odd[kRing][4];                 // values that are not finite, by tail tile
+    __shared__ int s_late;                               // a wait ran out
     __shared__ int s_acc[2];                             // a group's first product of a segment adds to O
     uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sQ = smem_u32(smem), sP = sQ + C::Q, sKV = sP + C::P, sV = sKV + C::KV_BYTES, sOut = sV + C::NV * C::SLOT;
     const uint32_t bFull = sOut + C::OUT, bEmpty = bFull + 8 * C::SLOTS;
     const uint32_t bVFull = bEmpty + 8 * C::SLOTS, bVEmpty = bVFull + 8 * C::NV;
     const uint32_t bS = bVEmpty + 8 * C::NV, bP = bS + 16, bO = bP + 16;
-    const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8, bDone = bQFree + 8;
+    const uint32_t bTail = bO + 16, bSeg = bTail + 8 * kRing, bSegFree = bSeg + 8 * kRing, bQ = bSegFree + 8 * kRing, bQFree = bQ + 8, bDone = bQFree + 8, bMeet = bDone + 8;
     // the ring of copies: keys in one slot, values in the next
     constexpr uint32_t slot_bytes = kTile * C::ROWB;
     constexpr int slots = C::SLOTS;
@@ -226,11 +245,14 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         bar_init(bQ, C::F8 || C::FEW ? C::QW : 32 * C::QW);
         bar_init(bQFree, 1);
         bar_init(bDone, 1);
+        s_late = 0;
+        bar_init(bMeet, kSoftWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_dependency_wait();
 
     // The requests' costs, their sum U, and this CTA's run of [0, U).
+    const long long began = clock64();
     int bits = 0;
     bool ok = true, led = true; // no wait for data, for a segment ran out
     const int per = (p.R + kGroup - 1) / kGroup;
@@ -309,6 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const uint8_t *cache = static_cast<const uint8_t *>(keys ? p.cache.k : p.cache.v) + 16 * (lane % C::CPR);
         Ring ring{keys ? 0 : 1, 0}, seg{0, 0};
         Split split0{}, split1{};
+        long long passed = began; // when the last segment was
         int i = 0, tails = 0; // tiles, tail tiles so far
         for (;;) {
             int nt, r, key0, end, h;
@@ -321,7 +344,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 h = walk.h;
                 const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
                 bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSegWaitNs);
-                __syncwarp();
+                const long long now = clock64();
+                led = __all_sync(~0u, led && now - passed < kPassClocks);
+                passed = now;
+                if (!led) // too late, or the slot is in use: nothing more is passed on
+                    break;
                 if (lane == 0) {
                     Seg &sg = s_seg[seg.s];
                     sg.nt = nt;
@@ -342,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 tails += max(0, nt - first_tail);
             } else {
                 bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
-                __syncwarp();
+                led = __all_sync(~0u, led);
                 nt = led ? s_seg[seg.s].nt : 0;
                 r = s_seg[seg.s].r;
                 key0 = s_seg[seg.s].key0;
@@ -489,19 +516,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         if (keys && lane < 2)
             static_cast<Split *>(p.workspace)[2 * blockIdx.x + lane] = lane ? split1 : split0;
         cp_async_wait_all();
-        if (box && !__all_sync(~0u, ok)) {
-            // a wait ran out: bulk copies that nothing waited for may be on their
-            // way still, and take microseconds
-            unsigned long long t0, t;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-            do
-                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-            while (t - t0 < kDrainNs);
-        }
     } else if (warp == kIssuer) {
         // ---- the products ------------------------------------------------
         constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
         const uint32_t lead = elect_lane(); // it issues, see mma_ss
+        const uint32_t lead_s = p.debug_withhold_scores ? 0u : lead;
         Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
         uint32_t q_ph = 0;
         int left = 0, nt = 0; // tiles of the segment without scores, all of them
@@ -548,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     mma_ss(d, dq, st, dk, st, idS, k > 0, lead);
                 }
             }
-            tc_commit(bS + 8 * buf, lead);
+            tc_commit(bS + 8 * buf, lead_s);
             if (!C::TWO || g == 1) {
                 tc_commit(bEmpty + 8 * kr.s, lead);
                 if (--left == 0)
@@ -646,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         int segs = 0;
         for (;;) {
             bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
-            __syncwarp();
+            led = __all_sync(~0u, led);
             if (!led || s_seg[seg.s].nt == 0)
                 break;
             const int tok = s_seg[seg.s].tok, n = s_seg[seg.s].n, h = s_seg[seg.s].h, g0 = s_seg[seg.s].rt * MT;
@@ -660,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 for (int k = 0; k < ALL; ++k) {
                     const int idx = ct + k * QT, qr = idx / CH, x = rem0 + qr;
                     const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
-                    const uint16_t *src = p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D + 8 * (idx % CH);
+                    const uint16_t *src = p.q + min(tok + ti, p.T - 1) * p.ld_q + (long long)(h * G + x - dt * G) * D + 8 * (idx % CH);
                     cp_async16_zfill(sQ + (qr >> 7) * C::Q1 + op_off(qr & 127, idx % CH), ti < n ? src : p.q, ti < n);
                 }
                 cp_async_arrive(bQ);
@@ -677,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         const int dt = G == 1 ? x : (int)__umulhi((uint32_t)x, inv_g), ti = t0 + dt;
                         v[k] = make_uint4(0u, 0u, 0u, 0u);
                         if (ti < n)
-                            v[k] = *reinterpret_cast<const uint4 *>(p.q + (tok + ti) * p.ld_q + (long long)(h * G + x - dt * G) * D +
+                            v[k] = *reinterpret_cast<const uint4 *>(p.q + min(tok + ti, p.T - 1) * p.ld_q + (long long)(h * G + x - dt * G) * D +
                                                                     8 * (idx % CH));
                     }
                     if (k0 == 0)
@@ -748,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         int i = 0;
         for (;;) {
             bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
-            __syncwarp();
+            led = __all_sync(~0u, led);
             const int nt = s_seg[seg.s].nt, first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
             const int key0 = s_seg[seg.s].key0, end = s_seg[seg.s].end, len = s_seg[seg.s].len;
             if (!led || nt == 0)
@@ -798,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     __syncwarp();
                     vs = smem + (sKV - sQ) + vr.s * slot_bytes;
                 }
-                const int tail = (tail_index + t - first_tail) % kRing;
+                const uint32_t tail = (uint32_t)(tail_index + t - first_tail) % kRing;
                 if (is_tail) {
                     // A tail tile: values behind the end become zero, and of the
                     // drafted tokens' those that are not finite are marked.
@@ -847,11 +866,26 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const int gtid = tid & (kGroup - 1);
         const float base_factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
         Ring seg{0, 0};
+        // The warps of a group, or with rows for both of both, meet: the latter by a wait
+        // like the others, since one that ran out may bring them there differently.
+        uint32_t meet_ph = 0;
+        auto meet = [&] {
+            if constexpr (C::TWO) {
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(bMeet);
+                bar_wait(bMeet, meet_ph, ok);
+                meet_ph ^= 1;
+                __syncwarp();
+            } else {
+                named_sync<kGroup>(2 + grp);
+            }
+        };
         uint32_t s_ph = 0; // of this group's next tile: S, P, O take the same turns
         int i0 = 0, segs = 0;
         for (;;) {
             bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
-            __syncwarp();
+            led = __all_sync(~0u, led);
             const Seg sg = s_seg[seg.s];
             if (!led || sg.nt == 0)
                 break;
@@ -1013,7 +1047,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     const int tail = sg.tail_index + t - sg.first_tail;
                     bar_wait(bTail + 8 * (tail % kRing), (tail / kRing) & 1, ok);
                     const uint32_t *odd = s_odd[tail % kRing];
-                    if (odd[0] | odd[1] | odd[2] | odd[3]) {
+                    // (One answer for all that meet below, also where the wait ran out: then
+                    // odd may change under the reads. With rows for both groups a barrier of
+                    // both here costs 12 wide trees 189 us against 184, so theirs is below.)
+                    const uint32_t some = odd[0] | odd[1] | odd[2] | odd[3];
+                    if (C::TWO ? some != 0 : named_or<kGroup>(2 + grp, some)) {
                         // Rare: what is not finite must not reach, times zero, the
                         // rows that do not see its key. It is added to O here, for
                         // the rows that do, and taken out of the slot.
@@ -1048,11 +1086,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                                 tmem_st16(tO + c, o);
                             }
                         tmem_st_wait();
-                        // every group that reads the slot has read it
-                        if constexpr (C::TWO)
-                            named_sync<2 * kGroup>(1);
-                        else
-                            named_sync<kGroup>(2 + grp);
+                        meet(); // every group that reads the slot has read it
                         if ((odd[wq] >> lane) & 1) {
                             constexpr uint16_t EXP = C::F8 ? 0x7c00 : 0x7f80;
                             for (int e = 0; e < D; ++e) {
@@ -1064,10 +1098,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                         if (gtid == 0)
                             s_acc[grp] = t < dt;
                         fence_async_smem();
-                        if constexpr (C::TWO)
-                            named_sync<2 * kGroup>(1);
-                        else
-                            named_sync<kGroup>(2 + grp);
+                        meet();
                     }
                 }
                 tc_before();
@@ -1241,11 +1272,23 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         }
     }
     tc_before();
-    if (!ok || !led)
+    if (!ok || !led) {
         set_status(p.status, SGQ_STATUS_TIMEOUT);
+        s_late = 1;
+    }
     __syncthreads();
-    if (warp == kIssuer)
+    if (warp == kIssuer) {
+        if (s_late) {
+            // bulk copies that nothing waited for may be on their way still, and take
+            // microseconds
+            unsigned long long t0, t;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+            do
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            while (t - t0 < kDrainNs);
+        }
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+    }
 }
 
 // Joins the parts of the items that several CTAs worked on, in key order. A unit

@@ -42,6 +42,7 @@ EXPORTS = (
     "sgq_ffn_workspace_bytes", "sgq_ffn", "sgq_read_status", "sgq_debug_gemv_withhold",
     "sgq_gemv_thresh_batch", "sgq_gemv_glu_thresh_batch", "sgq_cache_plan", "sgq_cache_write",
     "sgq_tree_attn_workspace_bytes", "sgq_tree_attn", "sgq_residual_norm",
+    "sgq_debug_tree_attn_withhold",
 )
 
 
@@ -114,6 +115,7 @@ def _declare(lib):
         "sgq_cache_write": ([P, L, P, L, P, L, I, P, I, P, P, I, P, P, L, P, P, P], I),
         "sgq_tree_attn_workspace_bytes": ([I, I, I, I, I], Z),
         "sgq_tree_attn": ([P, L, I, I, I, P, P, P, I, P, P, I, F, P, L, P, P, Z, P, P], I),
+        "sgq_debug_tree_attn_withhold": ([P, L, I, I, I, P, P, P, I, P, P, I, F, P, L, P, P, Z, P, P], I),
         "sgq_residual_norm": ([P, L, I, P, P, L, F, P, L, I, P, L, P, I, F, P, L, I, I, F, P], I),
         "sgq_status_string": ([I], ctypes.c_char_p),
         "sgq_last_cuda_error": ([], I),
@@ -448,8 +450,23 @@ def sgq_tree_attn_workspace_bytes(T: int, R: int, Hq: int, Hkv: int, D: int) -> 
 def sgq_tree_attn(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
                   scale, out, ld_out, lse, workspace, status=None, stream=None):
     """Attention of each request's new tokens over its pages of ``cache`` (a Cache)."""
+    _tree_attn("sgq_tree_attn", q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree,
+               tree_words, scale, out, ld_out, lse, workspace, status, stream)
+
+
+def sgq_debug_tree_attn_withhold(q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree,
+                                 tree_words, scale, out, ld_out, lse, workspace, status,
+                                 stream=None):
+    """Test hook: sgq_tree_attn whose scores are never passed on, so the
+    kernel's bounded waits run out and set SGQ_STATUS_TIMEOUT."""
+    _tree_attn("sgq_debug_tree_attn_withhold", q, ld_q, T, R, Hq, lens, cu_new, table, table_ld,
+               cache, tree, tree_words, scale, out, ld_out, lse, workspace, status, stream)
+
+
+def _tree_attn(name, q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
+               scale, out, ld_out, lse, workspace, status, stream):
     d = torch._C._cuda_getDevice()
-    _check("sgq_tree_attn", load().sgq_tree_attn(
+    _check(name, getattr(load(), name)(
         _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _I32, d),
         _dev("cu_new", cu_new, _I32, d), _dev("table", table, _I32, d), table_ld, cache.on(d),
         _dev("tree", tree, _I32, d), tree_words, scale, _dev("out", out, _BF16, d), ld_out,

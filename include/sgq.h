@@ -508,7 +508,9 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  * Any lengths and shares of Hq / heads, Hq <= 32768, T * Hq < 2^31,
  * table_ld * page <= 2^30. The grid depends on the arguments alone and nothing
  * is read back: a call can be captured and replayed on other lengths. The
- * kernel's waits are bounded by 0.2 s: SGQ_STATUS_TIMEOUT says that one ran out.
+ * kernel's waits are bounded by 0.2 s (2 s for a run's next part):
+ * SGQ_STATUS_TIMEOUT says that one ran out. The kernel then ends within
+ * seconds, the rows it had to write may hold anything, and no others do.
  */
 size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D);
 int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,
@@ -575,6 +577,19 @@ int sgq_debug_gemv_withhold(const void *qweight, const void *sz, int N, int K, i
                             const void *x, int B, const int32_t *idx, const int32_t *count,
                             void *y, float *y_f32, void *workspace, size_t ws_bytes,
                             int32_t *status, void *stream);
+
+/*
+ * The same for the attention kernel: sgq_tree_attn in which the commits that
+ * pass scores on to the softmax are withheld. The waits give up after 0.2 s,
+ * SGQ_STATUS_TIMEOUT is set in *status and out and lse are not valid; the call
+ * ends within seconds and the context stays usable. Arguments as sgq_tree_attn.
+ */
+int sgq_debug_tree_attn_withhold(const void *q, long long ld_q, int T, int R, int Hq,
+                                 const int32_t *lens, const int32_t *cu_new, const int32_t *table,
+                                 int table_ld, const sgq_cache *cache_host, const uint32_t *tree,
+                                 int tree_words, float scale, void *out, long long ld_out,
+                                 float *lse, void *workspace, size_t ws_bytes, int32_t *status,
+                                 void *stream);
 
 #ifdef __cplusplus
 }

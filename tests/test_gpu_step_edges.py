@@ -168,3 +168,22 @@ def test_attention_rows_of_q_that_are_not_finite(dtype, Hq, n, bad):
     assert torch.isnan(c.out[rows].float()).all() and not torch.isfinite(c.lse[rows]).any()
     c.q[rows] = 0                   # the oracle needs numbers there
     c.check(rows=[t for t in range(c.cu[-1]) if t not in rows])
+
+
+# ---- waits that run out ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page", [16, 3])                          # bulk copies, and others
+@pytest.mark.parametrize("Hq,n", [(4, 2), (8, 9), (8, 40)])
+def test_attention_wait_limits_set_timeout_and_the_context_survives(dtype, page, Hq, n):
+    # Host-side injection: the kernel's issuer never passes scores on, so the waits for them
+    # run out. The call returns, and the next one, on the same workspace, is right.
+    c = Attn([3000] + [40] * 30, [n] * 31, Hq, 1, 128, page, "nhd", dtype, "random", seed=n, rows=3)
+    a = c.args()
+    sgq.sgq_debug_tree_attn_withhold(**a)
+    torch.cuda.synchronize()
+    assert c.status.item() == sgq.SGQ_STATUS_TIMEOUT
+    n_rows = c.cu[-1]
+    assert (c.out[n_rows:] == 9.0).all() and (c.lse[n_rows:] == 9.0).all()
+    c.status.zero_()
+    c.run().check()
