@@ -61,13 +61,13 @@
 // as scores are one tile ahead of the products with the values: in a ring of an odd
 // number of slots the values two turns back are then used up before the keys between.
 //
-// Every wait for another warp's work is bounded by 0.2 s, for a segment and for its
-// slot by 2 s; one that runs out sets SGQ_STATUS_TIMEOUT, its warp waits for no data any
+// Every wait for another warp's work is bounded by 0.2 s, those for a segment, for its
+// slot and for the end of the last one's scores by 2 s and more for a long one; one that runs out sets SGQ_STATUS_TIMEOUT, its warp waits for no data any
 // more and the kernel comes to its end. The warps of a group also meet at barriers of
 // their own, which have no limit: they come to the same ones as long as they work on the
 // same segments, and they do whatever runs out, since the warp that passes segments on
-// stops for good kPassClocks after the last one, well before any other has waited for
-// 2 s (at 250 MHz and more). A segment's slot may then be written before every warp has
+// stops for good kPassClocks and more after the last one, well before any other has
+// waited that long (at 250 MHz and more). A segment's slot may then be written before every warp has
 // read it, so what they read there is kept in bounds field by field.
 #include "step_launch.cuh"
 #include "tc_device.cuh"
@@ -92,7 +92,9 @@ constexpr int kRing = 8;        // segments, and tail tiles, that are known to m
 constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
 constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 400000000ull;
-constexpr long long kPassClocks = 500000000; // see the segments' hand-over
+constexpr long long kPassClocks = 500000000; // see the top
+// What a tile may add to either: one takes 0.2 to 1.1 us, and a segment up to 2^23.
+constexpr unsigned kTileNs = 20000, kTileClocks = 5000;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
@@ -175,6 +177,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+
+// How long to wait for the segment behind one of nt tiles.
+__device__ __forceinline__ unsigned long long seg_wait(int nt) { return kSegWaitNs + (unsigned long long)nt * kTileNs; }
 
 // Byte offset of 16-byte chunk c of row r of an operand of 16-bit elements.
 __device__ __forceinline__ uint32_t op_off(int r, int c)
@@ -333,8 +338,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         Split split0{}, split1{};
         long long passed = began; // when the last segment was
         int i = 0, tails = 0; // tiles, tail tiles so far
+        int nt = 0;           // tiles of the segment
         for (;;) {
-            int nt, r, key0, end, h;
+            const int last_nt = nt;
+            int r, key0, end, h;
             if (keys) {
                 const bool more = __all_sync(~0u, ok) && walk.next(p, G, MT);
                 nt = more ? (walk.nu + 1) / 2 : 0;
@@ -343,9 +350,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 end = walk.key_end();
                 h = walk.h;
                 const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
-                bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSegWaitNs);
+                bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, seg_wait(last_nt));
                 const long long now = clock64();
-                led = __all_sync(~0u, led && now - passed < kPassClocks);
+                led = __all_sync(~0u, led && now - passed < kPassClocks + (long long)last_nt * kTileClocks);
                 passed = now;
                 if (!led) // too late, or the slot is in use: nothing more is passed on
                     break;
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 }
                 tails += max(0, nt - first_tail);
             } else {
-                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
                 led = __all_sync(~0u, led);
                 nt = led ? s_seg[seg.s].nt : 0;
                 r = s_seg[seg.s].r;
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         // Whether there is a next tile; its segment is looked up.
         auto next = [&]() -> bool {
             if (left == 0 && !ended) {
-                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(abs(nt)));
                 __syncwarp();
                 left = (int)__reduce_max_sync(~0u, __all_sync(~0u, led) ? (unsigned)s_seg[seg.s].nt : 0u);
                 seg.step(1, kRing);
@@ -662,18 +669,20 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const uint32_t inv_g = 0xffffffffu / (uint32_t)G + 1; // x / G = (x inv_g) >> 32 for x G < 2^32
         Ring seg{0, 0};
         uint32_t free_ph = 1; // the operand is free at first
-        int segs = 0;
+        int segs = 0, nt = 0;
         for (;;) {
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            const int last_nt = nt; // tiles of the segment that is worked on meanwhile
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
             led = __all_sync(~0u, led);
-            if (!led || s_seg[seg.s].nt == 0)
+            nt = s_seg[seg.s].nt;
+            if (!led || nt == 0)
                 break;
             const int tok = s_seg[seg.s].tok, n = s_seg[seg.s].n, h = s_seg[seg.s].h, g0 = s_seg[seg.s].rt * MT;
             seg.step(1, kRing);
             const int t0 = g0 / G, rem0 = g0 - t0 * G;
             if constexpr (!C::F8 && !C::FEW) {
                 // many rows: straight into their places
-                bar_wait(bQFree, free_ph, ok);
+                bar_wait(bQFree, free_ph, ok, seg_wait(last_nt));
                 __syncwarp();
 #pragma unroll 4
                 for (int k = 0; k < ALL; ++k) {
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                                                                     8 * (idx % CH));
                     }
                     if (k0 == 0)
-                        bar_wait(bQFree, free_ph, ok); // the last segment's scores are done
+                        bar_wait(bQFree, free_ph, ok, seg_wait(last_nt)); // the last segment's scores are done
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
@@ -764,11 +773,12 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         constexpr int VT = 32 * C::VW;
         const int ct = tid - 32 * C::kV;
         Ring seg{0, 0}, vr{C::F8 ? 1 : 0, 0};
-        int i = 0;
+        int i = 0, nt = 0;
         for (;;) {
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(nt));
             led = __all_sync(~0u, led);
-            const int nt = s_seg[seg.s].nt, first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
+            nt = s_seg[seg.s].nt;
+            const int first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
             const int key0 = s_seg[seg.s].key0, end = s_seg[seg.s].end, len = s_seg[seg.s].len;
             if (!led || nt == 0)
                 break;
@@ -882,9 +892,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             }
         };
         uint32_t s_ph = 0; // of this group's next tile: S, P, O take the same turns
-        int i0 = 0, segs = 0;
+        int i0 = 0, segs = 0, last_nt = 0;
         for (;;) {
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
             led = __all_sync(~0u, led);
             const Seg sg = s_seg[seg.s];
             if (!led || sg.nt == 0)
@@ -1268,6 +1278,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 bar_arrive(bSegFree + 8 * seg.s);
             seg.step(1, kRing);
             i0 += sg.nt;
+            last_nt = sg.nt;
             ++segs;
         }
     }

@@ -170,6 +170,37 @@ def test_attention_rows_of_q_that_are_not_finite(dtype, Hq, n, bad):
     c.check(rows=[t for t in range(c.cu[-1]) if t not in rows])
 
 
+# ---- runs of a second ----
+
+def test_attention_over_contexts_of_two_hundred_million_keys():
+    # Two contexts of 2^28 keys a SM, all of them 256 times over the one page there is (table
+    # rows may name a page again): each takes about half a second, longer than the limit
+    # of a wait for data. One key in 4096 counts, the others are 250 nats below.
+    R, page, D, times = 2 * torch.cuda.get_device_properties(0).multi_processor_count, 1 << 20, 64, 256
+    g = torch.Generator().manual_seed(1)
+    at = torch.arange(0, page, 4096)
+    keys, vals = torch.full((page, 1, D), -8.0), torch.ones(page, 1, D)
+    keys[at], vals[at] = 0.3 * torch.randn(len(at), 1, D, generator=g), torch.randn(len(at), 1, D, generator=g)
+    keys, vals = keys.to(BF16), vals.to(BF16)
+    q = (4 + 0.25 * torch.randn(R, 1, D, generator=g)).to(BF16)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    out, lse, status = torch.zeros(R, 1, D, dtype=BF16, device=DEV), torch.zeros(R, 1, device=DEV), i32([0])
+    sgq.sgq_tree_attn(q.to(DEV), D, R, R, 1, i32([times * page - 1] * R), i32(list(range(R + 1))),
+                      torch.zeros(R, times, dtype=torch.int32, device=DEV), times,
+                      sgq.Cache(keys[None].to(DEV), vals[None].to(DEV)), None, 0, D ** -0.5, out, D, lse,
+                      sgq.alloc_tree_attn_workspace(R, R, 1, 1, D), status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    k, v = keys[at].float().double(), vals[at].float().double()
+    ref, rl, mag, dots = so.attention_by_head(q, list(range(R + 1)), [k] * R, [v] * R, [torch.ones(1, len(at), dtype=torch.bool)] * R, D ** -0.5)
+    to, tl = so.attention_tolerance(ref, rl, mag, dots, D, 2.0 ** -8)
+    # 2^16 weights that are not zero are added one after the other, each time with one
+    # rounding of the sum so far: by half a step in l, by a whole one in the tensor core.
+    long = 2.0 ** 16 * so.U
+    assert ((out.cpu().double() - ref).abs() <= to + 3 * long * mag).all()
+    assert ((lse.cpu().double() - rl - math.log(times)).abs() <= tl + long).all()
+
+
 # ---- waits that run out ----
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
