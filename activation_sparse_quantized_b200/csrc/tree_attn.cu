@@ -88,6 +88,7 @@ constexpr float kGrowth = 8.0f; // binary orders a row's maximum may outgrow its
 // fp16 weights (8-bit caches) are 2^7 times the bf16 ones: up to 2^15 of fp16's 2^16, and so
 // with all the room below that there is (the sums l carry the same factor).
 constexpr float kLift16 = 7.0f;
+constexpr float kLeast = 1e-45f; // the smallest positive fp32 number
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
 constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
@@ -912,7 +913,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
             rq.n = sg.n;
             rq.len = sg.len;
             const uint64_t first = takes && sg.first_tail < sg.nt ? tree_bits(p, rq, tok_i) : 0;
-            float factor = fmaxf(base_factor, 1e-37f); // a scale of zero: all scores alike
+            // a scale of zero makes all scores alike: the least number there is, since zero
+            // times an unseen key's -infinity would be none
+            float factor = fmaxf(base_factor, kLeast);
             // the reference, as a score and in base 2, and the sum
             float ms = -INFINITY, m = -INFINITY, l = 0.0f;
 
@@ -926,7 +929,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     s_acc[grp] = 0;
                 if constexpr (C::F8)
                     if (t == t0)
-                        factor = fmaxf(base_factor * s_f[segs & 3][trow], 1e-37f);
+                        factor = fmaxf(base_factor * s_f[segs & 3][trow], kLeast);
                 // Tiles that reach the drafted tokens or the end, or hold a key
                 // without a page.
                 const uint32_t *bad = s_bad[(i0 + t) % kTiles];

@@ -110,6 +110,19 @@ def test_attention_scores_far_beyond_the_exponents_range(dtype, Hq, n, power):
     assert ((c.lse.cpu().double() - lse).abs() <= 2.0 ** -20 + 8 * so.U * lse.abs()).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,n", [(4, 2), (8, 9), (8, 40)])
+@pytest.mark.parametrize("scale", [0.0, 1e-38, -3e-39, 1e-35])
+def test_attention_scales_next_to_zero(dtype, Hq, n, scale):
+    # the products reach 2^117 (q 2^57 times k up to 2^53; 8-bit k up to 8 and q 2^110)
+    g = torch.Generator().manual_seed(n)
+    c = Attn([300], [n], Hq, 1, 64, 16, "nhd", dtype, None, seed=n)
+    c.put(0, torch.randint(-7, 8, (300 + n, 1, 64), generator=g).float() * (2.0 ** 50 if dtype == BF16 else 1.0))
+    c.q = (torch.randint(-7, 8, (n, Hq, 64), generator=g) * 2.0 ** (57 if dtype == BF16 else 107)).to(BF16)
+    c.scale = scale
+    c.run().check()
+
+
 # ---- weights far below the largest ----
 
 def share(c, R):
