@@ -9,7 +9,8 @@ import torch
 
 import step_oracle as so
 from activation_sparse_quantized_b200 import build, sgq
-from test_gpu_step import AttnCase
+from test_gpu_step import AttnCase, i32, make_cache, rope_table, status_word
+from test_gpu_step import test_write as check_write
 
 pytestmark = pytest.mark.gpu
 
@@ -196,7 +197,6 @@ def test_attention_over_contexts_of_two_hundred_million_keys():
     keys[at], vals[at] = 0.3 * torch.randn(len(at), 1, D, generator=g), torch.randn(len(at), 1, D, generator=g)
     keys, vals = keys.to(BF16), vals.to(BF16)
     q = (4 + 0.25 * torch.randn(R, 1, D, generator=g)).to(BF16)
-    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
     out, lse, status = torch.zeros(R, 1, D, dtype=BF16, device=DEV), torch.zeros(R, 1, device=DEV), i32([0])
     sgq.sgq_tree_attn(q.to(DEV), D, R, R, 1, i32([times * page - 1] * R), i32(list(range(R + 1))),
                       torch.zeros(R, times, dtype=torch.int32, device=DEV), times,
@@ -231,3 +231,53 @@ def test_attention_wait_limits_set_timeout_and_the_context_survives(dtype, page,
     assert (c.out[n_rows:] == 9.0).all() and (c.lse[n_rows:] == 9.0).all()
     c.status.zero_()
     c.run().check()
+
+
+# ---- a prompt's chunk ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("lens,news", [([0], [513]), ([777], [300]), ([50, 1030, 0, 3], [1, 1, 400, 1])])
+def test_attention_of_a_long_chain(dtype, lens, news):
+    Attn(lens, news, 8, 2, 128, 16, "hnd", dtype, None, seed=sum(news), rows=1).run().check()
+
+
+# ---- the store of many tokens ----
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,layout,dtype,rope", [
+    (296, 32, 8, 128, 16, "nhd", BF16, True), (700, 8, 2, 64, 24, "hnd", BF16, True), (513, 64, 8, 128, 64, "hnd", E4M3, True),
+    (1000, 6, 3, 64, 16, "nhd", E4M3, False), (301, 0, 2, 128, 8, "nhd", BF16, False), (600, 7, 1, 128, 7, "nhd", E4M3, True),
+    (299, 200, 40, 64, 16, "hnd", BF16, True)])
+def test_write_of_many_tokens(T, Hq, Hkv, D, page, layout, dtype, rope):
+    # several heads a thread, from 2 tokens a SM on
+    check_write(T, Hq, Hkv, D, page, layout, dtype, rope)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_write_of_many_tokens_skips_flags_and_writes_q_in_place(dtype):
+    # What few tokens and many are told to skip is the same, and the rest too: against calls
+    # of 100 rows each (a kernel of one head a thread) on the same values.
+    T, Hq, Hkv, D, page = 1000, 8, 2, 64, 16
+    pages = T // page + 2
+    g = torch.Generator().manual_seed(3)
+    qkv = (torch.randn(T, (Hq + 2 * Hkv) * D, generator=g) * 300).to(BF16)
+    qkv[5, 7], qkv[400, Hq * D + 3], qkv[401, -1] = math.nan, math.inf, -math.inf
+    slots, pos = torch.randperm(pages * page, generator=g)[:T], torch.randint(0, 50, (T,), generator=g, dtype=torch.int32)
+    slots[torch.arange(0, T, 9)] = -1
+    slots[123], slots[777] = pages * page, -2
+    pos[50], pos[600] = 50, -1
+    n, ld = 901, qkv.shape[1]
+    table, got = rope_table(50, D).to(DEV), []
+    for step in (T, 100):
+        k, v = make_cache(pages, page, Hkv, D, "nhd", dtype, 5.0)
+        cache, st = sgq.Cache(k, v, *((0.7, 1.3) if dtype == E4M3 else (1.0, 1.0))), status_word()
+        d, ds, dp = qkv.to(DEV), slots.to(DEV), pos.to(DEV)
+        for t in range(0, T, step):
+            rows = d[t:t + step]
+            sgq.sgq_cache_write(rows, ld, rows[:, Hq * D:], ld, rows[:, (Hq + Hkv) * D:], ld, step, i32([max(0, min(step, n - t))]), Hq,
+                                dp[t:], table, 50, ds[t:], rows, ld, cache, st)
+        torch.cuda.synchronize()
+        assert st.item() == sgq.SGQ_STATUS_BAD_INDEX
+        w = torch.uint8 if dtype == E4M3 else torch.int16
+        got.append((d.view(torch.int16), k.view(w), v.view(w)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(got[0][0][n:].cpu(), qkv[n:].view(torch.int16))       # rows behind the count
