@@ -13,12 +13,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libsgq.so")
+BINDING_SOURCE = os.path.join(CSRC, "tensors.cpp")
+BINDING_PATH = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-Xcompiler", "-fPIC",
@@ -42,6 +45,23 @@ def nvcc():
     return "nvcc"
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the binding's helper module (if stale) against this Python and torch."""
+    if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(BINDING_PATH) >= max(
+            os.path.getmtime(p) for p in (BINDING_SOURCE, __file__)):
+        return BINDING_PATH
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(at, "include"),
+           "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"), BINDING_SOURCE, "-o", BINDING_PATH + ".tmp",
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH
+
+
 def is_stale(out: str = LIB_PATH) -> bool:
     if not os.path.exists(out):
         return True
@@ -50,7 +70,9 @@ def is_stale(out: str = LIB_PATH) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, out: str = LIB_PATH) -> str:
-    """Compile every .cu under csrc/ into one shared library (if stale)."""
+    """Compile every .cu under csrc/ into one shared library (if stale), and the binding's helper."""
+    if out == LIB_PATH:
+        build_binding(force)
     if not force and not is_stale(out):
         return out
     cmd = [nvcc(), *ARCH, *FLAGS, "-I", INCLUDE, *sources(), "-o", out + ".tmp"]

@@ -132,9 +132,16 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current device and its current stream's handle, by torch's own short way where
+# this torch has it (building a Stream object takes 3 us).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream, dev=None):
-    if stream is None:  # the current stream's handle (building a torch Stream object takes 3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+    if stream is None:
+        return _current_stream(torch.cuda.current_device() if dev is None else dev)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -345,12 +352,14 @@ def sgq_glu(gate, up, h, B, I, act, stream=None):
 
 # --------------------------------------------------------------------------
 # The step around the projections: cache plan and store, tree attention, norm.
-# These wrappers check what the C ABI cannot see of a tensor: its element type
-# and that it lies on the current device.
+# These wrappers check what the C ABI cannot see of a tensor: its element type,
+# that it lies on the current device, that it is dense (rows: along a row), and
+# that it holds what the sizes say is read or written.
 # --------------------------------------------------------------------------
 
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 _FLOATS = {torch.bfloat16: SGQ_TYPE_BF16, torch.float32: SGQ_TYPE_F32}
+_OF_TYPE = (torch.bfloat16, torch.float32)  # by SGQ_TYPE_*
 _CACHES = {torch.bfloat16: SGQ_TYPE_BF16, torch.float8_e4m3fn: SGQ_TYPE_E4M3}
 
 
@@ -363,6 +372,60 @@ def _dev(name, t, dtype, dev):
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected the current device, cuda:{dev}")
     return t.data_ptr()
+
+
+def _dense(name, t, dtype, dev, need):
+    """The address of a dense tensor of at least ``need`` elements (None passes)."""
+    at = _dev(name, t, dtype, dev)
+    if t is not None:
+        if t.numel() < need:
+            raise ValueError(f"{name}: {t.numel()} elements, expected {need} at least")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: strides {t.stride()} of {tuple(t.shape)} are not dense")
+    return at
+
+
+def _rows(name, t, dtype, dev, rows, ld, width):
+    """The address of ``rows`` rows of ``width`` elements, ``ld`` apart, which may be a view of
+    wider ones (None passes)."""
+    at = _dev(name, t, dtype, dev)
+    if t is None:
+        return at
+    need = (rows - 1) * ld + width
+    if t.numel() >= need and t.is_contiguous():
+        return at
+    side = 1  # elements side by side so far, from the last dimension on
+    for n, stride in zip(reversed(t.shape), reversed(t.stride())):
+        if n > 1 and side < width and stride == side:
+            side *= n
+        elif n > 1:  # the rows
+            if stride != ld and (side < width or rows > 1 and ld):
+                raise ValueError(f"{name}: strides {t.stride()} of {tuple(t.shape)} are not those of dense rows, {ld} apart")
+            break
+    held = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if held < need:
+        raise ValueError(f"{name}: {held} elements, expected {rows} rows of {width}, {ld} apart")
+    return at
+
+
+_fast = None
+
+
+def _addresses(dev, names, tensors, types, sizes):
+    """The addresses of several tensors, each as from _dense (its size is a number) or from
+    _rows (rows, ld, width); by the module csrc/tensors.cpp in a tenth of the time, and here
+    where something is wrong, to say what (or where that module has not been built)."""
+    global _fast
+    if _fast is None:
+        try:
+            from ._tensors import addresses as _fast
+        except ImportError:
+            _fast = lambda *a: None  # noqa: E731
+    at = _fast(dev, tensors, types, sizes)
+    if at is None:
+        at = [_rows(name, t, dtype, dev, *n) if isinstance(n, tuple) else _dense(name, t, dtype, dev, n)
+              for name, t, dtype, n in zip(names, tensors, types, sizes)]
+    return at
 
 
 def _float_type(name, t):
@@ -416,30 +479,43 @@ class Cache:
         return self.ptr
 
 
+_PLAN = ("lens", "news", "table", "held", "held_out", "free_pages", "free_count", "free_count_out", "depth", "cu_new",
+         "slots", "pos", "req", "status")
+_PLAN_TYPES = (_I32,) * 10 + (_I64,) + (_I32,) * 3
+
+
 def sgq_cache_plan(lens, news, R, page, num_pages, table, table_ld, held, held_out, free_pages,
                    free_count, free_count_out, depth, max_tokens, cu_new, slots, pos, req,
                    status=None, stream=None):
     """Block tables, slots and positions of the requests' new tokens, on the GPU."""
-    d = torch._C._cuda_getDevice()
+    d = _current_device()
+    # (of depth as many are read as there are new tokens, which the device alone knows)
+    (lens, news, table, held, held_out, free_pages, free_count, free_count_out, depth, cu_new, slots, pos, req,
+     status) = _addresses(
+        d, _PLAN, (lens, news, table, held, held_out, free_pages, free_count, free_count_out, depth, cu_new, slots, pos,
+                   req, status), _PLAN_TYPES,
+        (R, R, (R, table_ld, table_ld), R, R, num_pages, 1, 1, 0, R + 1, max_tokens, max_tokens, max_tokens, 1))
     _check("sgq_cache_plan", load().sgq_cache_plan(
-        _dev("lens", lens, _I32, d), _dev("news", news, _I32, d), R, page, num_pages,
-        _dev("table", table, _I32, d), table_ld, _dev("held", held, _I32, d),
-        _dev("held_out", held_out, _I32, d), _dev("free_pages", free_pages, _I32, d),
-        _dev("free_count", free_count, _I32, d), _dev("free_count_out", free_count_out, _I32, d),
-        _dev("depth", depth, _I32, d), max_tokens, _dev("cu_new", cu_new, _I32, d),
-        _dev("slots", slots, _I64, d), _dev("pos", pos, _I32, d), _dev("req", req, _I32, d),
-        _dev("status", status, _I32, d), _stream(stream, d)))
+        lens, news, R, page, num_pages, table, table_ld, held, held_out, free_pages, free_count, free_count_out, depth,
+        max_tokens, cu_new, slots, pos, req, status, _stream(stream, d)))
+
+
+_WRITE = ("q", "k", "v", "n_tokens", "pos", "rope", "slots", "q_out", "status")
+_WRITE_TYPES = (_BF16, _BF16, _BF16, _I32, _I32, _F32, _I64, _BF16, _I32)
 
 
 def sgq_cache_write(q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_len, slots,
                     q_out, ld_qo, cache, status=None, stream=None):
     """Rotate q and k by position; q to q_out, k and v into their slots of ``cache`` (a Cache)."""
-    d = torch._C._cuda_getDevice()
+    d = _current_device()
+    dim = cache.struct.dim
+    kv = cache.struct.heads * dim
+    q, k, v, n_tokens, pos, rope, slots, q_out, status = _addresses(
+        d, _WRITE, (q, k, v, n_tokens, pos, rope, slots, q_out, status), _WRITE_TYPES,
+        ((T, ld_q, Hq * dim), (T, ld_k, kv), (T, ld_v, kv), 1, 0 if rope is None else T, rope_len * dim, T,
+         (T, ld_qo, Hq * dim), 1))
     _check("sgq_cache_write", load().sgq_cache_write(
-        _dev("q", q, _BF16, d), ld_q, _dev("k", k, _BF16, d), ld_k, _dev("v", v, _BF16, d), ld_v,
-        T, _dev("n_tokens", n_tokens, _I32, d), Hq, _dev("pos", pos, _I32, d),
-        _dev("rope", rope, _F32, d), rope_len, _dev("slots", slots, _I64, d),
-        _dev("q_out", q_out, _BF16, d), ld_qo, cache.on(d), _dev("status", status, _I32, d),
+        q, ld_q, k, ld_k, v, ld_v, T, n_tokens, Hq, pos, rope, rope_len, slots, q_out, ld_qo, cache.on(d), status,
         _stream(stream, d)))
 
 
@@ -463,33 +539,42 @@ def sgq_debug_tree_attn_withhold(q, ld_q, T, R, Hq, lens, cu_new, table, table_l
                cache, tree, tree_words, scale, out, ld_out, lse, workspace, status, stream)
 
 
+_ATTN = ("q", "lens", "cu_new", "table", "tree", "out", "lse", "workspace", "status")
+_ATTN_TYPES = (_BF16, _I32, _I32, _I32, _I32, _BF16, _F32, _I32, _I32)
+
+
 def _tree_attn(name, q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
                scale, out, ld_out, lse, workspace, status, stream):
-    d = torch._C._cuda_getDevice()
+    d = _current_device()
+    width, ws_bytes = Hq * cache.struct.dim, 0 if workspace is None else workspace.nbytes
+    q, lens, cu_new, table, tree, out, lse, workspace, status = _addresses(
+        d, _ATTN, (q, lens, cu_new, table, tree, out, lse, workspace, status),
+        _ATTN_TYPES,
+        ((T, ld_q, width), R, R + 1, (R, table_ld, table_ld), (T, tree_words, tree_words), (T, ld_out, width), T * Hq, 0, 1))
     _check(name, getattr(load(), name)(
-        _dev("q", q, _BF16, d), ld_q, T, R, Hq, _dev("lens", lens, _I32, d),
-        _dev("cu_new", cu_new, _I32, d), _dev("table", table, _I32, d), table_ld, cache.on(d),
-        _dev("tree", tree, _I32, d), tree_words, scale, _dev("out", out, _BF16, d), ld_out,
-        _dev("lse", lse, _F32, d), _dev("workspace", workspace, _I32, d),
-        0 if workspace is None else workspace.nbytes,
-        _dev("status", status, _I32, d), _stream(stream, d)))
+        q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache.on(d), tree, tree_words, scale, out, ld_out, lse, workspace,
+        ws_bytes, status, _stream(stream, d)))
+
+
+_NORM = ("a", "w_post", "gate", "resid", "resid_out", "w_pre", "x")
 
 
 def sgq_residual_norm(a, ld_a, w_post, gate, ld_gate, scale, resid, ld_r, resid_out, ld_ro,
                       w_pre, w_offset, x, ld_x, B, H, eps, stream=None):
     """The norms around a block with its gate and scaled residual; the element
     types of the C entry point (a_type, r_type, w_type) are the tensors' own."""
-    d = torch._C._cuda_getDevice()
+    d = _current_device()
     w = w_pre if w_pre is not None else w_post if w_post is not None else gate
-    at, rt = None if a is None else a.dtype, None if resid is None else resid.dtype
-    wt = None if w is None else w.dtype
+    at = SGQ_TYPE_F32 if a is None else _float_type("a", a)
+    rt = SGQ_TYPE_F32 if resid is None else _float_type("resid", resid)
+    wt = SGQ_TYPE_F32 if w is None else _float_type("w_pre, w_post and gate", w)
+    r, ws = _OF_TYPE[rt], _OF_TYPE[wt]
+    a, w_post, gate, resid, resid_out, w_pre, x = _addresses(
+        d, _NORM, (a, w_post, gate, resid, resid_out, w_pre, x), (_OF_TYPE[at], ws, ws, r, r, ws, _BF16),
+        ((B, ld_a, H), H, (B, ld_gate, H), (B, ld_r, H), (B, ld_ro, H), H, (B, ld_x, H)))
     _check("sgq_residual_norm", load().sgq_residual_norm(
-        _dev("a", a, at, d), ld_a, SGQ_TYPE_F32 if a is None else _float_type("a", a),
-        _dev("w_post", w_post, wt, d), _dev("gate", gate, wt, d), ld_gate, scale,
-        _dev("resid", resid, rt, d), ld_r, SGQ_TYPE_F32 if resid is None else _float_type("resid", resid),
-        _dev("resid_out", resid_out, rt, d), ld_ro, _dev("w_pre", w_pre, wt, d),
-        SGQ_TYPE_F32 if w is None else _float_type("w_pre, w_post and gate", w), w_offset,
-        _dev("x", x, _BF16, d), ld_x, B, H, eps, _stream(stream, d)))
+        a, ld_a, at, w_post, gate, ld_gate, scale, resid, ld_r, rt, resid_out, ld_ro, w_pre, wt, w_offset, x, ld_x, B, H,
+        eps, _stream(stream, d)))
 
 
 # --------------------------------------------------------------------------
