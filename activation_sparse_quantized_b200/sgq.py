@@ -541,6 +541,7 @@ def sgq_debug_tree_attn_withhold(q, ld_q, T, R, Hq, lens, cu_new, table, table_l
 
 _ATTN = ("q", "lens", "cu_new", "table", "tree", "out", "lse", "workspace", "status")
 _ATTN_TYPES = (_BF16, _I32, _I32, _I32, _I32, _BF16, _F32, _I32, _I32)
+_ATTN_TYPES_U32 = (_BF16, _I32, _I32, _I32, torch.uint32, _BF16, _F32, _I32, _I32)
 
 
 def _tree_attn(name, q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tree, tree_words,
@@ -549,7 +550,7 @@ def _tree_attn(name, q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache, tr
     width, ws_bytes = Hq * cache.struct.dim, 0 if workspace is None else workspace.nbytes
     q, lens, cu_new, table, tree, out, lse, workspace, status = _addresses(
         d, _ATTN, (q, lens, cu_new, table, tree, out, lse, workspace, status),
-        _ATTN_TYPES,
+        _ATTN_TYPES_U32 if tree is not None and tree.dtype is torch.uint32 else _ATTN_TYPES,
         ((T, ld_q, width), R, R + 1, (R, table_ld, table_ld), (T, tree_words, tree_words), (T, ld_out, width), T * Hq, 0, 1))
     _check(name, getattr(load(), name)(
         q, ld_q, T, R, Hq, lens, cu_new, table, table_ld, cache.on(d), tree, tree_words, scale, out, ld_out, lse, workspace,

@@ -180,6 +180,14 @@ def test_one_gate_for_all_rows(calls):
         sgq.sgq_residual_norm(**dict(a, gate=torch.zeros(16, dtype=BF16).expand(3, 16)))
 
 
+def test_tree_words_of_either_type(calls):
+    a = attn_call_args()
+    for t in (I32, torch.uint32):
+        sgq.sgq_tree_attn(**dict(a, tree=torch.zeros(a["T"], 1, dtype=t)))
+    with pytest.raises(TypeError, match="^tree: "):
+        sgq.sgq_tree_attn(**dict(a, tree=torch.zeros(a["T"], 1, dtype=I64)))
+
+
 def test_the_helper_module_refuses_what_is_no_call():
     from activation_sparse_quantized_b200 import _tensors
     t = torch.zeros(4, dtype=I32)
