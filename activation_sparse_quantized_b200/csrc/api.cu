@@ -146,7 +146,7 @@ const char *sgq_status_string(int code)
     case SGQ_ERR_SHAPE: return "shape out of range or not divisible as required";
     case SGQ_ERR_GROUP: return "group size must be 32, 64 or 128";
     case SGQ_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
-    case SGQ_ERR_BATCH: return "batch must be between 1 and 16";
+    case SGQ_ERR_BATCH: return "batch outside 1..16, or number of requests outside 1..8192";
     case SGQ_ERR_WORKSPACE: return "workspace smaller than the entry point's *_workspace_bytes";
     case SGQ_ERR_ACT: return "unknown activation";
     case SGQ_ERR_CUDA: return "a CUDA call failed (see sgq_last_cuda_error)";

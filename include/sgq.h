@@ -52,8 +52,8 @@ extern "C" {
 #define SGQ_ERR_SHAPE      -2  /* N, K, B or a size out of range / indivisible   */
 #define SGQ_ERR_GROUP      -3  /* group size not 32, 64 or 128                   */
 #define SGQ_ERR_ALIGN      -4  /* a device pointer is not 16-byte aligned        */
-#define SGQ_ERR_BATCH      -5  /* B < 1 or B > SGQ_MAX_BATCH                     */
-#define SGQ_ERR_WORKSPACE  -6  /* workspace smaller than sgq_gemv_workspace_bytes */
+#define SGQ_ERR_BATCH      -5  /* B outside 1..SGQ_MAX_BATCH, R outside 1..SGQ_MAX_REQUESTS */
+#define SGQ_ERR_WORKSPACE  -6  /* workspace smaller than the entry point's *_workspace_bytes */
 #define SGQ_ERR_ACT        -7  /* unknown activation                             */
 #define SGQ_ERR_CUDA       -8  /* a CUDA runtime call or launch failed           */
 #define SGQ_ERR_DEVICE     -9  /* current device is not compute capability 10.x  */

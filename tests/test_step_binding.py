@@ -22,6 +22,12 @@ def test_the_attention_test_hook_refuses_what_the_entry_point_refuses(lib, fault
     assert lib.sgq_debug_tree_attn_withhold(*attn_args(lib, **fault)) == code
 
 
+def test_a_number_of_requests_out_of_range_is_called_that(lib):
+    assert lib.sgq_tree_attn(*attn_args(lib, R=8193)) == -5
+    words = lib.sgq_status_string(-5)
+    assert b"requests" in words and str(sgq.SGQ_MAX_REQUESTS).encode() in words and str(sgq.SGQ_MAX_BATCH).encode() in words
+
+
 class Recorder:
     """Stands in for the library: takes every call and keeps its arguments."""
 
