@@ -206,7 +206,9 @@ size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D)
     if (T < 1 || R < 1 || R > SGQ_MAX_REQUESTS || Hkv < 1 || Hq < Hkv || Hq > 32768 || Hq % Hkv != 0 ||
         (D != 64 && D != 128))
         return 0;
-    return sgq::attn_workspace_bytes(T, R, Hq, Hkv, D);
+    // Fewer requests have more rows each and may need a larger row tile: what T rows of
+    // one request need is enough for up to T rows of any number.
+    return sgq::attn_workspace_bytes(T, 1, Hq, Hkv, D);
 }
 
 int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,

@@ -489,9 +489,10 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  *   scale     finite (|scale| k_scale <= 1e37), of either sign.
  *   out       bf16 [T][Hq][dim], rows ld_out apart, not q. lse: optional fp32
  *             [T][Hq].
- *   workspace sgq_tree_attn_workspace_bytes bytes for these T, R, Hq, heads and
- *             dim, any content; it holds nothing between calls. Calls that may
- *             overlap must not share one.
+ *   workspace sgq_tree_attn_workspace_bytes bytes for these Hq, heads and dim and
+ *             a T and R that are these or more (a call with fewer rows or requests
+ *             never needs a larger one), any content; it holds nothing between
+ *             calls. Calls that may overlap must not share one.
  * A token that sees no key, or none with a score above -infinity, has out = 0
  * and lse = -infinity. Of a row of q with an infinity or NaN out is NaN with an
  * SGQ_TYPE_E4M3 cache, and what its scores make it with a bf16 one; other rows

@@ -1,6 +1,8 @@
 """The step entry points' binding: what it refuses of tensors, on the host, and the
 calls around the entry points (no GPU needed: CPU tensors and a recording library
 stand in for the device's)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -26,6 +28,24 @@ def test_a_number_of_requests_out_of_range_is_called_that(lib):
     assert lib.sgq_tree_attn(*attn_args(lib, R=8193)) == -5
     words = lib.sgq_status_string(-5)
     assert b"requests" in words and str(sgq.SGQ_MAX_REQUESTS).encode() in words and str(sgq.SGQ_MAX_BATCH).encode() in words
+
+
+@pytest.mark.parametrize("Hq,heads,dim", [(32, 8, 128), (8, 8, 64), (128, 2, 128)])
+def test_a_workspace_for_the_largest_step_takes_every_smaller_one(lib, Hq, heads, dim):
+    sizes = [1, 2, 5, 16, 40, 64, 300, 8192]
+    small = dict(k=1 << 20, v=1 << 21, type=0, page=16, num_pages=64, heads=heads, dim=dim, page_stride=16 * heads * dim,
+                 slot_stride=heads * dim, head_stride=dim, k_scale=1.0, v_scale=1.0)
+    c = ctypes.byref(sgq._CacheStruct(*[small[f] for f, _ in sgq._CacheStruct._fields_]))
+    for T in sizes:
+        for R in sizes:
+            ws = lib.sgq_tree_attn_workspace_bytes(T, R, Hq, heads, dim)
+            for t in sizes[:sizes.index(T) + 1]:
+                for r in sizes[:sizes.index(R) + 1]:
+                    # no GPU here: a call that passes its checks fails later, for another reason
+                    a = attn_args(lib, T=t, R=r, Hq=Hq, ld_q=Hq * dim, ld_out=Hq * dim, cache=c, wsb=ws, status=None)
+                    assert ws >= lib.sgq_tree_attn_workspace_bytes(t, r, Hq, heads, dim)
+                    if not torch.cuda.is_available():
+                        assert lib.sgq_tree_attn(*a) in (-8, -9), (T, R, t, r)
 
 
 class Recorder:
