@@ -44,8 +44,8 @@ int check_cache(const sgq_cache *c)
         return SGQ_ERR_SHAPE;
     if (c->page_stride % unit || c->slot_stride % unit || c->head_stride % unit)
         return SGQ_ERR_ALIGN;
-    // heads, slots and pages of dim elements each may not overlap: a dimension
-    // of more than one entry steps over at least one row
+    // a dimension of more than one entry steps over at least one row of dim elements
+    // (that no two of them share elements otherwise is the caller's)
     if ((c->heads > 1 && c->head_stride < c->dim) || (c->page > 1 && c->slot_stride < c->dim) ||
         (c->num_pages > 1 && c->page_stride < c->dim))
         return SGQ_ERR_SHAPE;

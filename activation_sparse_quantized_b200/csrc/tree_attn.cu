@@ -24,8 +24,8 @@
 //    and bad pages, is filled with zeros. The copies are bulk tensor copies, a
 //    box per 128 bytes of so many slots of a page, where a box has 512 bytes at
 //    least, else cp.async of 16 bytes a lane. A box takes its warp some 40 ns
-//    (11 requests of 8-bit keys in pages of 24, 16 boxes of 512 bytes a slot: 75 us,
-//    in pages of 128 70);
+//    (11 requests of 8-bit keys in pages of 24, 16 boxes of 512 bytes a slot: 79 us,
+//    in pages of 128 75);
 //  * one thread issues S = Q K^T (both from shared memory) into one of two
 //    accumulators, one tile ahead and across segments, and O += P V with P
 //    read from tensor memory, where it takes S's place;
@@ -48,13 +48,13 @@
 // whatever lies there, and so are those of O).
 //
 // What bounds it: with few rows and 16-bit keys memory (24 requests of 16000 keys
-// and more, 32 query and 8 key heads of 128: 246 to 253 us, 6.2 to 6.4 TB/s), with
-// 8-bit ones the products' reads of shared memory and the hand-offs; with 512 rows
-// a request the chain of a tile, scores, exponentials, products (12 requests of up
-// to 16384 keys, 64 / 8 heads of 128: 164 us, 618 TFLOP/s). Slower there: scores in
-// halves of 64 keys, one with the softmax while the next are computed (171); 64
-// scores in registers at a time (177), and the other warps' registers for them
-// (187). Slower with few rows: scores two tiles ahead (75 us against 54 on 24
+// and more, 32 query and 8 key heads of 128: 255 to 290 us as the clocks are, 5.4 to
+// 6.2 TB/s), with 8-bit ones the products' reads of shared memory and the hand-offs;
+// with 512 rows a request the chain of a tile, scores, exponentials, products (12
+// requests of up to 16384 keys, 64 / 8 heads of 128: 176 to 192 us, 530 to 575
+// TFLOP/s). Slower there: scores in halves of 64 keys, one with the softmax while the
+// next are computed (by 4%); 64 scores in registers at a time (8%), and the other warps'
+// registers for them (14%). Slower with few rows: scores two tiles ahead (by 38% on 24
 // requests of up to 16111 keys), for which the ring holds too little.
 //
 // The copies' ring tells a slot's phases by their parity alone. That holds as long
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 // 2^-14, 2^-25, which is 2^-32 of the row's largest at most); their
                 // sum l is of the unrounded ones.
                 // (A third of the exponentials by polynomial on the FMA pipe did
-                // not change 12 wide trees' 175 us, half of them made it 184.)
+                // not change 12 wide trees' time, half of them made it 5% longer.)
                 // The reference is taken off as a score, before the factor: in base 2 it is
                 // rounded, and from 2^28 on by more than the weights' type can take. (That is an
                 // addition per pair of scores: 191.5 us against 188.6 on 12 wide trees, 77.1
@@ -1457,9 +1457,10 @@ cudaError_t launch_t(const AttnProblem &p, int grid, cudaStream_t stream)
 {
     using C = Cfg<D, KV, MT>;
     // Bulk copies where a box, the largest power of two up to 64 slots that
-    // divides the page, has kBoxBytes at least: 84 us against 88 on 11 requests
-    // of up to 60000 8-bit keys in pages of 24 (boxes of 512 bytes), 72 against
-    // 83 on 24 ragged ones in pages of 32 (boxes of 4 KB).
+    // divides the page, has kBoxBytes at least: 79 us against 88 by cp.async on 11
+    // requests of up to 60000 8-bit keys in pages of 24 (boxes of 512 bytes), 61 against
+    // 86 on 24 ragged ones in pages of 32 (boxes of 4 KB); with pages of 12 (boxes of
+    // 256 bytes) 103 against 96.
     int box = 1;
     while (box < 64 && p.cache.page % (2 * box) == 0)
         box *= 2;

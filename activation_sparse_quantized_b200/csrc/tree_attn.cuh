@@ -10,8 +10,9 @@ namespace sgq {
 namespace {
 
 constexpr int kBN = 64;        // keys per unit
-constexpr int kItemCost = 5;   // what an item costs beside its units, in units (measured: 24 ragged requests
-                               // take 69, 61, 55 and 55 us with 1, 2, 4 and 8)
+constexpr int kItemCost = 5;   // what an item costs beside its units, in units (measured with 1, 2, 4, 5 and 8:
+                               // 24 ragged requests take 76, 69, 62, 61 and 60 us, 11 of 8-bit keys 92, 87,
+                               // 80, 79 and 80, 300 of up to 400 keys 102, 102, 105, 105 and 107)
 constexpr int kMaxGrid = 160;  // one CTA per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

@@ -397,7 +397,8 @@ typedef struct sgq_cache {
     int heads;         /* kv heads                                                    */
     int dim;           /* 64 or 128                                                   */
     long long page_stride, slot_stride, head_stride; /* elements; multiples of 16 bytes,
-                          up to 2^38, and at least dim where there is more than one  */
+                          up to 2^38, and at least dim where there is more than one;
+                          no two rows of dim elements may share any                  */
     float k_scale, v_scale; /* 1 for SGQ_TYPE_BF16, finite and > 0 for SGQ_TYPE_E4M3 */
 } sgq_cache;
 
