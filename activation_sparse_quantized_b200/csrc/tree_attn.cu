@@ -61,14 +61,15 @@
 // as scores are one tile ahead of the products with the values: in a ring of an odd
 // number of slots the values two turns back are then used up before the keys between.
 //
-// Every wait for another warp's work is bounded by 0.2 s, those for a segment, for its
-// slot and for the end of the last one's scores by 2 s and more for a long one; one that runs out sets SGQ_STATUS_TIMEOUT, its warp waits for no data any
-// more and the kernel comes to its end. The warps of a group also meet at barriers of
-// their own, which have no limit: they come to the same ones as long as they work on the
-// same segments, and they do whatever runs out, since the warp that passes segments on
-// stops for good kPassClocks and more after the last one, well before any other has
-// waited that long (at 250 MHz and more). A segment's slot may then be written before every warp has
-// read it, so what they read there is kept in bounds field by field.
+// Every wait for another warp's work is bounded, by 0.2 s for data and by 90 s for the
+// next segment and for the end of one's scores, which may take 10 s; one that runs out
+// sets SGQ_STATUS_TIMEOUT, its warp waits for no data any more and the kernel comes to its
+// end, which is passed on as the last segment. The warps of a group also meet at barriers
+// of their own, which have no limit: they come to the same ones as long as they work on
+// the same segments, and they do whatever runs out, since the warp that passes segments on
+// stops for good kPassClocks after the last one, before any other has waited for 90 s (at
+// 250 MHz and more). A segment's slot may then be written before every warp has read it,
+// so what they read there is kept in bounds field by field.
 #include "step_launch.cuh"
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
@@ -92,10 +93,9 @@ constexpr float kLeast = 1e-45f; // the smallest positive fp32 number
 constexpr int kRing = 8;        // segments, and tail tiles, that are known to more than one warp
 constexpr int kBoxBytes = 512;  // smallest box of a bulk copy
 constexpr int kTiles = 16;      // tiles that are
-constexpr unsigned long long kSegWaitNs = 2000000000ull, kDrainNs = 400000000ull;
-constexpr long long kPassClocks = 500000000; // see the top
-// What a tile may add to either: one takes 0.2 to 1.1 us, and a segment up to 2^23.
-constexpr unsigned kTileNs = 20000, kTileClocks = 5000;
+// Limits, see the top. A segment has up to 2^23 tiles, which take up to 2200 clocks each.
+constexpr long long kPassClocks = 20000000000; // from one segment passed on to the next
+constexpr unsigned long long kSegWaitNs = 90000000000ull, kSlotWaitNs = 2000000000ull, kDrainNs = 400000000ull;
 
 template <int D_, int KV, int MT_>
 struct Cfg {
@@ -103,6 +103,13 @@ struct Cfg {
     static constexpr bool F8 = KV == SGQ_TYPE_E4M3, TWO = MT == 256, FEW = MT == 32;
     static constexpr int QW = F8 && !TWO ? 1 : 2, VW = !F8 ? 1 : TWO ? 2 : 4; // warps for Q, for the values read
     static constexpr int kV = kQ + QW, THREADS = 32 * (kV + VW);
+    // Whether what takes the softmax's warps to the barriers of the rare path is voted on at
+    // one. (With 16-bit keys and rows for both groups, whom that would bring together at
+    // every tail tile, they meet by waits like the others instead, which one that ran out
+    // may bring them to differently: 12 wide trees 184 us against 189; with 8-bit keys the
+    // vote is better, 257 against 268.)
+    static constexpr bool VOTE = !TWO || F8;
+    static constexpr int MEET = TWO ? 2 * kGroup : kGroup;    // threads that meet there
     static constexpr int ROWS = FEW ? 32 : 128;               // of a group
     static constexpr int COPIES = 128 / ROWS;                 // of the rows, in Q
     static constexpr int SUB = kTile * 128;                   // 128 rows x 128 bytes, swizzled
@@ -178,9 +185,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-
-// How long to wait for the segment behind one of nt tiles.
-__device__ __forceinline__ unsigned long long seg_wait(int nt) { return kSegWaitNs + (unsigned long long)nt * kTileNs; }
 
 // Byte offset of 16-byte chunk c of row r of an operand of 16-bit elements.
 __device__ __forceinline__ uint32_t op_off(int r, int c)
@@ -258,7 +262,6 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
     grid_dependency_wait();
 
     // The requests' costs, their sum U, and this CTA's run of [0, U).
-    const long long began = clock64();
     int bits = 0;
     bool ok = true, led = true; // no wait for data, for a segment ran out
     const int per = (p.R + kGroup - 1) / kGroup;
@@ -337,12 +340,10 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const uint8_t *cache = static_cast<const uint8_t *>(keys ? p.cache.k : p.cache.v) + 16 * (lane % C::CPR);
         Ring ring{keys ? 0 : 1, 0}, seg{0, 0};
         Split split0{}, split1{};
-        long long passed = began; // when the last segment was
+        long long passed = clock64(); // when the last segment was
         int i = 0, tails = 0; // tiles, tail tiles so far
-        int nt = 0;           // tiles of the segment
         for (;;) {
-            const int last_nt = nt;
-            int r, key0, end, h;
+            int nt, r, key0, end, h;
             if (keys) {
                 const bool more = __all_sync(~0u, ok) && walk.next(p, G, MT);
                 nt = more ? (walk.nu + 1) / 2 : 0;
@@ -351,9 +352,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 end = walk.key_end();
                 h = walk.h;
                 const int first_tail = max(0, (min(walk.rq.len, end) - key0) / kTile);
-                bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, seg_wait(last_nt));
+                bar_wait(bSegFree + 8 * seg.s, seg.ph ^ 1, led, kSlotWaitNs);
                 const long long now = clock64();
-                led = __all_sync(~0u, led && now - passed < kPassClocks + (long long)last_nt * kTileClocks);
+                led = __all_sync(~0u, led && now - passed < kPassClocks);
                 passed = now;
                 if (!led) // too late, or the slot is in use: nothing more is passed on
                     break;
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 }
                 tails += max(0, nt - first_tail);
             } else {
-                bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
                 led = __all_sync(~0u, led);
                 nt = led ? s_seg[seg.s].nt : 0;
                 r = s_seg[seg.s].r;
@@ -528,7 +529,6 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         // ---- the products ------------------------------------------------
         constexpr uint32_t idS = idesc_f16(!C::F8, false, kTile), idO = idesc_f16(!C::F8, true, D);
         const uint32_t lead = elect_lane(); // it issues, see mma_ss
-        const uint32_t lead_s = p.debug_withhold_scores ? 0u : lead;
         Ring kr{0, 0}, vr{1, 0}, seg{0, 0};
         uint32_t q_ph = 0;
         int left = 0, nt = 0; // tiles of the segment without scores, all of them
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         // Whether there is a next tile; its segment is looked up.
         auto next = [&]() -> bool {
             if (left == 0 && !ended) {
-                bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(abs(nt)));
+                bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
                 __syncwarp();
                 left = (int)__reduce_max_sync(~0u, __all_sync(~0u, led) ? (unsigned)s_seg[seg.s].nt : 0u);
                 seg.step(1, kRing);
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     mma_ss(d, dq, st, dk, st, idS, k > 0, lead);
                 }
             }
-            tc_commit(bS + 8 * buf, lead_s);
+            tc_commit(bS + 8 * buf, p.debug_withhold_scores ? 0u : lead);
             if (!C::TWO || g == 1) {
                 tc_commit(bEmpty + 8 * kr.s, lead);
                 if (--left == 0)
@@ -670,20 +670,18 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const uint32_t inv_g = 0xffffffffu / (uint32_t)G + 1; // x / G = (x inv_g) >> 32 for x G < 2^32
         Ring seg{0, 0};
         uint32_t free_ph = 1; // the operand is free at first
-        int segs = 0, nt = 0;
+        int segs = 0;
         for (;;) {
-            const int last_nt = nt; // tiles of the segment that is worked on meanwhile
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
             led = __all_sync(~0u, led);
-            nt = s_seg[seg.s].nt;
-            if (!led || nt == 0)
+            if (!led || s_seg[seg.s].nt == 0)
                 break;
             const int tok = s_seg[seg.s].tok, n = s_seg[seg.s].n, h = s_seg[seg.s].h, g0 = s_seg[seg.s].rt * MT;
             seg.step(1, kRing);
             const int t0 = g0 / G, rem0 = g0 - t0 * G;
             if constexpr (!C::F8 && !C::FEW) {
                 // many rows: straight into their places
-                bar_wait(bQFree, free_ph, ok, seg_wait(last_nt));
+                bar_wait(bQFree, free_ph, ok, kSegWaitNs);
                 __syncwarp();
 #pragma unroll 4
                 for (int k = 0; k < ALL; ++k) {
@@ -710,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                                                                     8 * (idx % CH));
                     }
                     if (k0 == 0)
-                        bar_wait(bQFree, free_ph, ok, seg_wait(last_nt)); // the last segment's scores are done
+                        bar_wait(bQFree, free_ph, ok, kSegWaitNs); // the last segment's scores are done
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
@@ -774,12 +772,11 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         constexpr int VT = 32 * C::VW;
         const int ct = tid - 32 * C::kV;
         Ring seg{0, 0}, vr{C::F8 ? 1 : 0, 0};
-        int i = 0, nt = 0;
+        int i = 0;
         for (;;) {
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(nt));
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
             led = __all_sync(~0u, led);
-            nt = s_seg[seg.s].nt;
-            const int first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
+            const int nt = s_seg[seg.s].nt, first_tail = s_seg[seg.s].first_tail, tail_index = s_seg[seg.s].tail_index;
             const int key0 = s_seg[seg.s].key0, end = s_seg[seg.s].end, len = s_seg[seg.s].len;
             if (!led || nt == 0)
                 break;
@@ -877,25 +874,24 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
         const int gtid = tid & (kGroup - 1);
         const float base_factor = fabsf(p.scale) * p.cache.k_scale * kLog2e;
         Ring seg{0, 0};
-        // The warps of a group, or with rows for both of both, meet: the latter by a wait
-        // like the others, since one that ran out may bring them there differently.
+        // The warps of a group, or with rows for both of both, meet.
         uint32_t meet_ph = 0;
         auto meet = [&] {
-            if constexpr (C::TWO) {
+            if constexpr (C::VOTE) {
+                named_sync<C::MEET>(C::TWO ? 1 : 2 + grp);
+            } else {
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(bMeet);
                 bar_wait(bMeet, meet_ph, ok);
                 meet_ph ^= 1;
                 __syncwarp();
-            } else {
-                named_sync<kGroup>(2 + grp);
             }
         };
         uint32_t s_ph = 0; // of this group's next tile: S, P, O take the same turns
-        int i0 = 0, segs = 0, last_nt = 0;
+        int i0 = 0, segs = 0;
         for (;;) {
-            bar_wait(bSeg + 8 * seg.s, seg.ph, led, seg_wait(last_nt));
+            bar_wait(bSeg + 8 * seg.s, seg.ph, led, kSegWaitNs);
             led = __all_sync(~0u, led);
             const Seg sg = s_seg[seg.s];
             if (!led || sg.nt == 0)
@@ -1061,10 +1057,9 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     bar_wait(bTail + 8 * (tail % kRing), (tail / kRing) & 1, ok);
                     const uint32_t *odd = s_odd[tail % kRing];
                     // (One answer for all that meet below, also where the wait ran out: then
-                    // odd may change under the reads. With rows for both groups a barrier of
-                    // both here costs 12 wide trees 189 us against 184, so theirs is below.)
+                    // odd may change under the reads.)
                     const uint32_t some = odd[0] | odd[1] | odd[2] | odd[3];
-                    if (C::TWO ? some != 0 : named_or<kGroup>(2 + grp, some)) {
+                    if (C::VOTE ? named_or<C::MEET>(C::TWO ? 1 : 2 + grp, some) : some != 0) {
                         // Rare: what is not finite must not reach, times zero, the
                         // rows that do not see its key. It is added to O here, for
                         // the rows that do, and taken out of the slot.
@@ -1281,7 +1276,6 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                 bar_arrive(bSegFree + 8 * seg.s);
             seg.step(1, kRing);
             i0 += sg.nt;
-            last_nt = sg.nt;
             ++segs;
         }
     }

@@ -510,10 +510,9 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  * Any lengths and shares of Hq / heads, Hq <= 32768, T * Hq < 2^31,
  * table_ld * page <= 2^30. The grid depends on the arguments alone and nothing
  * is read back: a call can be captured and replayed on other lengths. The
- * kernel's waits are bounded, by 0.2 s for data and by 2 s and 20 us for each
- * 128 keys of one head for the next head's: SGQ_STATUS_TIMEOUT says that one ran
- * out. The kernel then comes to its end, the rows it had to write may hold
- * anything, and no others do.
+ * kernel's waits are bounded, by 0.2 s for data and by 90 s for the end of one
+ * head's keys: SGQ_STATUS_TIMEOUT says that one ran out. The kernel then comes to
+ * its end, the rows it had to write may hold anything, and no others do.
  */
 size_t sgq_tree_attn_workspace_bytes(int T, int R, int Hq, int Hkv, int D);
 int sgq_tree_attn(const void *q, long long ld_q, int T, int R, int Hq, const int32_t *lens,
