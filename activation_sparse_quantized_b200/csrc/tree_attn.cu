@@ -48,11 +48,12 @@
 // whatever lies there, and so are those of O).
 //
 // What bounds it: with few rows and 16-bit keys memory (24 requests of 16000 keys
-// and more, 32 query and 8 key heads of 128: 255 to 290 us as the clocks are, 5.4 to
-// 6.2 TB/s), with 8-bit ones the products' reads of shared memory and the hand-offs;
-// with 512 rows a request the chain of a tile, scores, exponentials, products (12
-// requests of up to 16384 keys, 64 / 8 heads of 128: 176 to 192 us, 530 to 575
-// TFLOP/s). Slower there: scores in halves of 64 keys, one with the softmax while the
+// and more, 32 query and 8 key heads of 128: 255 us at full clock, 285 to 295 under the
+// power limit, 6.2 and 5.4 TB/s), with 8-bit ones a tile's copies, conversion, scores,
+// weights and products one after the other (11 requests of up to 60000 keys, 32 / 8
+// heads of 64: 78 us, 0.85 us a tile); with 512 rows a request the chain of scores,
+// exponentials, products (12 requests of up to 16384 keys, 64 / 8 heads of 128: 163 us at
+// full clock, 186 under the power limit, 622 and 545 TFLOP/s). Slower there: scores in halves of 64 keys, one with the softmax while the
 // next are computed (by 4%); 64 scores in registers at a time (8%), and the other warps'
 // registers for them (14%). Slower with few rows: scores two tiles ahead (by 38% on 24
 // requests of up to 16111 keys), for which the ring holds too little.
