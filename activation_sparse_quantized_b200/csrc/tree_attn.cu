@@ -962,7 +962,8 @@ __global__ void __launch_bounds__(Cfg<D, KV, MT>::THREADS, 1)
                     if (__any_sync(~0u, grow)) {
                         const float corr = grow ? exp2_fast((ms - top) * factor) : 1.0f;
                         ms = grow ? top : ms;
-                        m = grow ? top * factor : m;
+                        // (a score that leaves fp32 there is no reference: what follows is NaN)
+                        m = grow ? top * factor == -INFINITY ? NAN : top * factor : m;
                         l *= corr;
                         if (t >= dt && quad == 0) { // this group's last product is done: S was issued after it
 #pragma unroll 1

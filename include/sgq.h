@@ -502,7 +502,8 @@ int sgq_cache_write(const void *q, long long ld_q, const void *k, long long ld_k
  * Rows of no request are left as they were. A page outside [0, num_pages) is
  * skipped, its keys unseen, and sets SGQ_STATUS_BAD_INDEX; lengths and rows
  * outside the buffers' sizes are clamped and set SGQ_STATUS_BAD_COUNT.
- * Scores, maxima, sums and accumulators are fp32; the weights are rounded to
+ * Scores, maxima, sums and accumulators are fp32 (a row whose largest score times
+ * log2 e is beyond its range is NaN); the weights are rounded to
  * bf16 for their product with the values, with an SGQ_TYPE_E4M3 cache to fp16:
  * those below 2^-21 of their row's largest are then off by up to 2^-32 of it.
  * With an SGQ_TYPE_E4M3 cache q enters its product as the sum of two 8-bit

@@ -113,6 +113,26 @@ def test_attention_scores_far_beyond_the_exponents_range(dtype, Hq, n, power):
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("Hq,n", [(4, 2), (8, 9), (8, 40)])
+def test_attention_rows_whose_scores_leave_fp32_are_not_finite(dtype, Hq, n):
+    # Products of 9 x 64 x 2^117 and a scale of 8: 2^129 and more, in base 2. Row 0's are all
+    # above the range, row 1's all below it; the others are ordinary. The context is cut into
+    # parts, one key head to many SMs.
+    c = Attn([20000, 200], [n, n], Hq, 1, 64, 16, "nhd", dtype, None, seed=n)
+    keys = [k.clone() for k in c.keys]
+    for r in range(2):
+        keys[r][:] = 3.0
+        c.put(r, keys[r])
+    c.q = c.q * 2.0 ** -10
+    c.q[0], c.q[1] = 3 * 2.0 ** 117, -3 * 2.0 ** 117
+    c.scale = 8.0
+    c.run()
+    assert torch.isnan(c.out[:2].float()).all() and not torch.isfinite(c.lse[:2]).any()
+    c.q[:2] = 0                     # the oracle needs scores there
+    c.check(rows=list(range(2, c.cu[-1])))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,n", [(4, 2), (8, 9), (8, 40)])
 @pytest.mark.parametrize("scale", [0.0, 1e-38, -3e-39, 1e-35])
 def test_attention_scales_next_to_zero(dtype, Hq, n, scale):
     # the products reach 2^117 (q 2^57 times k up to 2^53; 8-bit k up to 8 and q 2^110)
