@@ -53,10 +53,11 @@
 // weights and products one after the other (11 requests of up to 60000 keys, 32 / 8
 // heads of 64: 78 us, 0.85 us a tile); with 512 rows a request the chain of scores,
 // exponentials, products (12 requests of up to 16384 keys, 64 / 8 heads of 128: 163 us at
-// full clock, 186 under the power limit, 622 and 545 TFLOP/s). Slower there: scores in halves of 64 keys, one with the softmax while the
-// next are computed (by 4%); 64 scores in registers at a time (8%), and the other warps'
-// registers for them (14%). Slower with few rows: scores two tiles ahead (by 38% on 24
-// requests of up to 16111 keys), for which the ring holds too little.
+// full clock, 186 under the power limit, 622 and 545 TFLOP/s). Slower there: scores in
+// halves of 64 keys, one with the softmax while the next are computed (by 4%); 64 scores
+// in registers at a time (8%), and the other warps' registers for them (14%). Slower with
+// few rows: scores two tiles ahead (by 38% on 24 requests of up to 16111 keys), for which
+// the ring holds too little.
 //
 // The copies' ring tells a slot's phases by their parity alone. That holds as long
 // as scores are one tile ahead of the products with the values: in a ring of an odd

@@ -301,3 +301,28 @@ def test_write_of_many_tokens_skips_flags_and_writes_q_in_place(dtype):
         got.append((d.view(torch.int16), k.view(w), v.view(w)))
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert torch.equal(got[0][0][n:].cpu(), qkv[n:].view(torch.int16))       # rows behind the count
+
+
+# ---- padded batches ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [60, 300])
+def test_attention_of_a_batch_padded_behind(dtype, rows):
+    # many rows behind the last request: the rows a request has on average, and so the row
+    # tile, are not what the requests have
+    Attn([500, 0, 33], [3, 1, 2], 8, 2, 128, 16, "nhd", dtype, "random", seed=rows, rows=rows).run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_attention_of_a_batch_padded_in_front(dtype):
+    c = Attn([300, 5], [4, 9], 8, 2, 64, 16, "nhd", dtype, "random", seed=4)
+    pad = 5
+    c.q = torch.cat([torch.full((pad, 8, 64), math.nan, dtype=BF16), c.q])
+    c.tree = torch.cat([torch.full((pad, c.words), 7), c.tree])
+    c.T += pad
+    out, lse = torch.full((c.T, 8, 64), 9.0, dtype=BF16, device=DEV), torch.full((c.T, 8), 9.0, device=DEV)
+    c.ws = sgq.alloc_tree_attn_workspace(c.T, 2, 8, 2, 64)
+    c.run(cu_new=i32([t + pad for t in c.cu]), out=out, lse=lse)
+    assert (out[:pad] == 9.0).all() and (lse[:pad] == 9.0).all()
+    c.q, c.out, c.lse = c.q[pad:], out[pad:], lse[pad:]
+    c.check()
