@@ -9,7 +9,7 @@ import torch
 
 import step_oracle as so
 from activation_sparse_quantized_b200 import build, sgq
-from test_gpu_step import AttnCase, i32, make_cache, rope_table, status_word
+from test_gpu_step import AttnCase, check_plan, i32, make_cache, plan_case, rope_table, run_plan, status_word
 from test_gpu_step import test_write as check_write
 
 pytestmark = pytest.mark.gpu
@@ -326,3 +326,34 @@ def test_attention_of_a_batch_padded_in_front(dtype):
     assert (out[:pad] == 9.0).all() and (lse[:pad] == 9.0).all()
     c.q, c.out, c.lse = c.q[pad:], out[pad:], lse[pad:]
     c.check()
+
+
+# ---- plans of many tokens (a second kernel writes the tokens' rows) ----
+
+@pytest.mark.parametrize("fault", ["short", "len", "new", "held", "wide", "tokens", "count", "page"])
+def test_plan_of_many_tokens_with_bad_state_or_too_few_pages(fault):
+    lens, news, page, pages, table, held, free, count = plan_case(900, 8, 1, 60, 40, 5, short=fault == "short")
+    T, r = sum(news), 333
+    if fault == "len":
+        lens[r] = -4
+    elif fault == "new":
+        news[r] = -1
+    elif fault == "held":
+        held[r] = 0
+    elif fault == "wide":
+        more = 8 * len(table[0]) + 1 - news[r]
+        news[r], T = news[r] + more, T + more
+    elif fault == "tokens":
+        T -= 4001
+    elif fault == "count":
+        count = pages + 50
+        free = free[:pages] + [0] * (pages - len(free[:pages]))
+    elif fault == "page":
+        r = next(i for i in range(r, 900) if lens[i] % 8 and news[i])
+        table[r][lens[r] // 8] = pages + 3
+    assert T > 8192
+    depth = [i % 5 for i in range(T + 3)] if fault in ("short", "page") else None
+    _, got = run_plan(lens, news, page, pages, table, held, free, count, depth, T, rows=T + 3)
+    want = so.plan(lens, news, page, pages, table, len(table[0]), held, free, count, depth, T)
+    assert want[-1]
+    check_plan(got, want, T)
